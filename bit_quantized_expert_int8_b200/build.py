@@ -15,7 +15,7 @@ FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "4",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 

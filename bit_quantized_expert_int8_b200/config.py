@@ -31,6 +31,18 @@ class MoeConfig:
         return replace(self, **kw)
 
 
+@dataclass(frozen=True)
+class KvConfig:
+    """Shape of a 4-bit KV cache and of the calls on it (pages of 64 entries)."""
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int               # 64, 128, 192 or 256
+    n_pages: int                # pages in the pool
+    max_pages: int              # pages of one sequence at most
+    max_seqs: int = 1           # sequences per call
+    max_rows: int = 1           # rows per call
+
+
 # Workload presets (synthetic inputs; recipes in the generator module).
 TINY = MoeConfig(H=256, E=16, k=2, I=128, Is=256)          # one layer, 1 token
 LAYER = MoeConfig()                                         # one layer, batch 1

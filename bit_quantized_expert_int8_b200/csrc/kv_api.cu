@@ -1,0 +1,279 @@
+// kv_api.cu -- the C ABI of the 4-bit KV cache (declared in moeq4.h): argument
+// checks, workspace and launches.  The arithmetic runs in kv_cache.cuh and
+// kv_attn.cuh.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+#include <new>
+
+#include "common.cuh"
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
+
+using namespace moeq4;
+
+// the library's per-thread error message (moe_last_error)
+void moeq4_set_error(const char* msg);
+
+static int kv_fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    moeq4_set_error(buf);
+    return code;
+}
+
+#define KV_CK(call)                                                                \
+    do {                                                                           \
+        cudaError_t e_ = (call);                                                   \
+        if (e_ != cudaSuccess)                                                     \
+            return kv_fail(MOE_ERR_CUDA, "%s: %s (%s:%d)", #call, cudaGetErrorString(e_), \
+                           __FILE__, __LINE__);                                    \
+    } while (0)
+
+#define KV_TRY(expr)                   \
+    do {                               \
+        int rc_ = (expr);              \
+        if (rc_ != MOE_OK) return rc_; \
+    } while (0)
+
+static inline bool kv_al(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+struct moe_kv {
+    MoeKvConfig cfg{};
+    int device = 0;
+    int n_sms = 0;
+    size_t smem_optin = 0;
+    uint8_t* ws = nullptr;
+    int* status = nullptr;
+    float* lse = nullptr;      // [max_rows][n_q_heads], where the caller wants none
+};
+
+static int kv_check_cfg(const MoeKvConfig* c) {
+    if (!c) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_create: cfg is NULL");
+    if (c->head_dim < 64 || c->head_dim > 256 || c->head_dim % 64)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64, 128, 192 or 256 (%d)", c->head_dim);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 128 || c->n_q_heads < 1 || c->n_q_heads > 1024 ||
+        c->n_q_heads % c->n_kv_heads)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE,
+                       "need 1 <= n_kv_heads <= 128 and n_q_heads <= 1024 a multiple of it (%d, %d)",
+                       c->n_kv_heads, c->n_q_heads);
+    if (c->n_pages < 1 || c->max_pages < 1 || c->max_pages > 32768)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "need n_pages >= 1 and max_pages in 1..32768");
+    if (c->max_seqs < 1 || c->max_seqs > 4096 || c->max_rows < 1 || c->max_rows > (1 << 20))
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "need max_seqs in 1..4096 and max_rows in 1..1048576");
+    if (c->reserved != 0) return kv_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");
+    return MOE_OK;
+}
+
+extern "C" size_t moe_kv_page_bytes(int n_kv_heads, int head_dim) {
+    if (n_kv_heads < 1 || n_kv_heads > 128 || head_dim < 64 || head_dim > 256 || head_dim % 64) return 0;
+    return (size_t)n_kv_heads * KvTile(head_dim / 64).bytes();
+}
+
+extern "C" int moe_kv_destroy(moe_kv* kv) {
+    if (!kv) return MOE_OK;
+    int dev = -1;
+    cudaGetDevice(&dev);
+    cudaSetDevice(kv->device);
+    cudaDeviceSynchronize();
+    if (kv->ws) cudaFree(kv->ws);
+    if (dev >= 0) cudaSetDevice(dev);
+    delete kv;
+    return MOE_OK;
+}
+
+extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
+    if (!out) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_create: out is NULL");
+    *out = nullptr;
+    KV_TRY(kv_check_cfg(cfg));
+    moe_kv* kv = new (std::nothrow) moe_kv();
+    if (!kv) return kv_fail(MOE_ERR_CUDA, "moe_kv_create: out of host memory");
+    kv->cfg = *cfg;
+    int optin = 0;
+    cudaError_t e = cudaGetDevice(&kv->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&kv->n_sms, cudaDevAttrMultiProcessorCount, kv->device);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, kv->device);
+    kv->smem_optin = (size_t)optin;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t o = off; off = (off + bytes + 255) / 256 * 256; return o; };
+    const size_t o_status = take(sizeof(int));
+    const size_t o_lse = take((size_t)cfg->max_rows * cfg->n_q_heads * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
+    if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
+    // every kernel's shared memory limit is raised here: no later call changes it
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    if (e != cudaSuccess) {
+        const int rc = kv_fail(MOE_ERR_CUDA, "moe_kv_create: %s", cudaGetErrorString(e));
+        moe_kv_destroy(kv);
+        return rc;
+    }
+    kv->status = reinterpret_cast<int*>(kv->ws + o_status);
+    kv->lse = reinterpret_cast<float*>(kv->ws + o_lse);
+    *out = kv;
+    return MOE_OK;
+}
+
+extern "C" int moe_kv_check(moe_kv* kv, moe_stream_t stream) {
+    if (!kv) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_check: NULL context");
+    KV_CK(cudaStreamSynchronize(stream));
+    int st = 0;
+    KV_CK(cudaMemcpy(&st, kv->status, sizeof(int), cudaMemcpyDeviceToHost));
+    if (st == 0) return MOE_OK;
+    KV_CK(cudaMemset(kv->status, 0, sizeof(int)));
+    return kv_fail(st, "a KV cache kernel met a length, row start or page index outside its limits");
+}
+
+static int kv_check_device(const moe_kv* kv, const char* who) {
+    int dev = -1;
+    KV_CK(cudaGetDevice(&dev));
+    if (dev != kv->device)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: the context belongs to device %d, current is %d", who, kv->device, dev);
+    return MOE_OK;
+}
+
+static int kv_check_cache(const moe_kv* kv, const MoeKvCache* c, int n_seqs, const char* who) {
+    if (!c->pages || !c->page_table || !c->lens) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL cache buffer", who);
+    if (!kv_al(c->pages, 16)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: pages must be 16-byte aligned", who);
+    if (!kv_al(c->page_table, 4) || !kv_al(c->lens, 4) || !kv_al(c->score, 4) || !kv_al(c->pos, 4) ||
+        !kv_al(c->seen, 4))
+        return kv_fail(MOE_ERR_ALIGNMENT, "%s: misaligned cache buffer", who);
+    if (c->pos && !c->seen) return kv_fail(MOE_ERR_INVALID_ARG, "%s: pos needs seen", who);
+    if (n_seqs < 0 || n_seqs > kv->cfg.max_seqs)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: n_seqs=%d outside 0..%d", who, n_seqs, kv->cfg.max_seqs);
+    return MOE_OK;
+}
+
+static int kv_check_batch(const moe_kv* kv, const MoeKvBatch* b, const char* who) {
+    if (!b->row_start || !kv_al(b->row_start, 4))
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: row_start is NULL or misaligned", who);
+    if (b->n_rows < 0 || b->n_rows > kv->cfg.max_rows)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: n_rows=%d outside 0..%d", who, b->n_rows, kv->cfg.max_rows);
+    if (b->max_q < 1) return kv_fail(MOE_ERR_INVALID_ARG, "%s: max_q must be >= 1", who);
+    if (b->reserved != 0) return kv_fail(MOE_ERR_INVALID_ARG, "%s: reserved must be zero", who);
+    return MOE_OK;
+}
+
+static int kv_check_rows(const void* p, int64_t stride, int heads, int D, const char* who) {
+    if (!p) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL rows", who);
+    if (!kv_al(p, 16)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: rows must be 16-byte aligned", who);
+    if (stride < (int64_t)heads * D || stride % 8 || stride > (int64_t)1 << 32)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: row stride %lld must be a multiple of 8, at least %d", who,
+                       (long long)stride, heads * D);
+    return MOE_OK;
+}
+
+static KvArgs kv_args(const moe_kv* kv, const MoeKvCache* c, const MoeKvBatch* b, int n_seqs) {
+    KvArgs a{};
+    a.pages = static_cast<uint8_t*>(c->pages);
+    a.table = c->page_table;
+    a.lens = c->lens;
+    a.row_start = b ? b->row_start : nullptr;
+    a.score = c->score;
+    a.pos = c->pos;
+    a.seen = c->seen;
+    a.status = kv->status;
+    a.n_seqs = n_seqs;
+    a.n_rows = b ? b->n_rows : 0;
+    a.max_q = b ? (b->max_q < b->n_rows ? b->max_q : b->n_rows) : 0;
+    a.hq = kv->cfg.n_q_heads;
+    a.hkv = kv->cfg.n_kv_heads;
+    a.ng = kv->cfg.head_dim / 64;
+    a.n_pages = kv->cfg.n_pages;
+    a.max_pages = kv->cfg.max_pages;
+    return a;
+}
+
+static int kv_rows_call(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* batch, moe_half* k,
+                        int64_t k_stride, moe_half* v, int64_t v_stride, bool read, cudaStream_t s) {
+    const char* who = read ? "moe_kv_read_q4" : "moe_kv_append_q4";
+    if (!kv || !cache || !batch) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL argument", who);
+    if (batch->n_seqs == 0 || batch->n_rows == 0) return MOE_OK;
+    KV_TRY(kv_check_cache(kv, cache, batch->n_seqs, who));
+    KV_TRY(kv_check_batch(kv, batch, who));
+    KV_TRY(kv_check_rows(k, k_stride, kv->cfg.n_kv_heads, kv->cfg.head_dim, who));
+    KV_TRY(kv_check_rows(v, v_stride, kv->cfg.n_kv_heads, kv->cfg.head_dim, who));
+    KV_TRY(kv_check_device(kv, who));
+    const KvArgs a = kv_args(kv, cache, batch, batch->n_seqs);
+    __half* kp = reinterpret_cast<__half*>(k);
+    __half* vp = reinterpret_cast<__half*>(v);
+    if (read) k_kv_rows<true><<<batch->n_rows, kKvRowThreads, 0, s>>>(a, kp, k_stride, vp, v_stride);
+    else k_kv_rows<false><<<batch->n_rows, kKvRowThreads, 0, s>>>(a, kp, k_stride, vp, v_stride);
+    KV_CK(cudaGetLastError());
+    return MOE_OK;
+}
+
+extern "C" int moe_kv_append_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* batch,
+                                const moe_half* k, int64_t k_stride, const moe_half* v,
+                                int64_t v_stride, moe_stream_t stream) {
+    return kv_rows_call(kv, cache, batch, const_cast<moe_half*>(k), k_stride, const_cast<moe_half*>(v),
+                        v_stride, false, stream);
+}
+
+extern "C" int moe_kv_read_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* batch, moe_half* k,
+                              int64_t k_stride, moe_half* v, int64_t v_stride, moe_stream_t stream) {
+    return kv_rows_call(kv, cache, batch, k, k_stride, v, v_stride, true, stream);
+}
+
+extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* batch,
+                           const moe_half* q, int64_t q_stride, float scale, int window, int flags,
+                           moe_half* out, int64_t out_stride, float* lse, moe_stream_t stream) {
+    const char* who = "moe_attn_q4";
+    if (!kv || !cache || !batch) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL argument", who);
+    if (batch->n_seqs == 0 || batch->n_rows == 0) return MOE_OK;
+    KV_TRY(kv_check_cache(kv, cache, batch->n_seqs, who));
+    KV_TRY(kv_check_batch(kv, batch, who));
+    KV_TRY(kv_check_rows(q, q_stride, kv->cfg.n_q_heads, kv->cfg.head_dim, who));
+    KV_TRY(kv_check_rows(out, out_stride, kv->cfg.n_q_heads, kv->cfg.head_dim, who));
+    if (flags & ~MOE_ATTN_WEIGHTS) return kv_fail(MOE_ERR_INVALID_ARG, "%s: unknown flags 0x%x", who, flags);
+    if (window < 0) return kv_fail(MOE_ERR_INVALID_ARG, "%s: window must be >= 0", who);
+    if (!std::isfinite(scale)) return kv_fail(MOE_ERR_INVALID_ARG, "%s: scale must be finite", who);
+    if ((flags & MOE_ATTN_WEIGHTS) && !cache->score)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: MOE_ATTN_WEIGHTS needs cache->score", who);
+    if (!kv_al(lse, 4)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: misaligned lse", who);
+    KV_TRY(kv_check_device(kv, who));
+    AttnArgs a{};
+    a.c = kv_args(kv, cache, batch, batch->n_seqs);
+    a.q = reinterpret_cast<const __half*>(q);
+    a.out = reinterpret_cast<__half*>(out);
+    a.lse = lse ? lse : kv->lse;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.scale = scale;
+    a.window = window;
+    k_attn_simple<<<dim3(batch->n_rows, a.c.hq), 256, 0, stream>>>(a);
+    KV_CK(cudaGetLastError());
+    if (flags & MOE_ATTN_WEIGHTS) {
+        k_attn_weights_simple<<<dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream>>>(a);
+        KV_CK(cudaGetLastError());
+    }
+    return MOE_OK;
+}
+
+extern "C" int moe_kv_evict(moe_kv* kv, const MoeKvCache* cache, int n_seqs, int budget, int n_recent,
+                            int32_t* new_lens, moe_stream_t stream) {
+    const char* who = "moe_kv_evict";
+    if (!kv || !cache) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL argument", who);
+    if (n_seqs == 0) return MOE_OK;
+    if (!new_lens) return kv_fail(MOE_ERR_INVALID_ARG, "%s: NULL argument", who);
+    KV_TRY(kv_check_cache(kv, cache, n_seqs, who));
+    if (!cache->score || !cache->pos || !cache->seen)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: needs score, pos and seen", who);
+    if (!kv_al(new_lens, 4)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: misaligned new_lens", who);
+    if (budget < 1 || n_recent < 0 || n_recent > budget)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: need 0 <= n_recent <= budget, budget >= 1", who);
+    if (new_lens < cache->lens + n_seqs && cache->lens < new_lens + n_seqs)
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: new_lens overlaps lens", who);
+    const size_t smem = evict_smem(kv->cfg.max_pages * kKvPage);
+    if (kv->cfg.max_pages > 8192 || smem > kv->smem_optin)
+        return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: max_pages=%d above 8192", who, kv->cfg.max_pages);
+    KV_TRY(kv_check_device(kv, who));
+    const KvArgs a = kv_args(kv, cache, nullptr, n_seqs);
+    k_kv_evict<<<dim3(a.hkv, n_seqs), kEvictThreads, smem, stream>>>(a, budget, n_recent, new_lens);
+    KV_CK(cudaGetLastError());
+    return MOE_OK;
+}

@@ -12,7 +12,7 @@ import os
 
 import torch
 
-from .config import MoeConfig
+from .config import KvConfig, MoeConfig
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoeq4.so")
@@ -27,6 +27,8 @@ MOE_ERR_CACHE_STATE = -6
 MOE_PRENORM = 1
 MOE_DEVICE_FILL = 2
 MOE_MAX_SLOTS = 32
+MOE_KV_PAGE = 64
+MOE_ATTN_WEIGHTS = 1
 
 EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_ctx_check", "moe_ctx_trace", "moe_ctx_info",
            "moe_last_error", "moe_blob_bytes",
@@ -35,7 +37,9 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_ctx_check", "moe_ctx_trace"
            "moe_cache_lookup_lfu", "moe_layer_decode", "moe_stack_decode",
            "moe_router_topk_noalloc", "moe_set_mma_min_tokens", "moe_set_wait_ns",
            "moe_store_stride", "moe_store_open", "moe_store_close", "moe_store_read",
-           "moe_store_stats")
+           "moe_store_stats",
+           "moe_kv_page_bytes", "moe_kv_create", "moe_kv_destroy", "moe_kv_check",
+           "moe_kv_append_q4", "moe_kv_read_q4", "moe_attn_q4", "moe_kv_evict")
 
 
 class MoeError(RuntimeError):
@@ -72,6 +76,20 @@ class CMoeLfuTable(ctypes.Structure):
                 ("valid", ctypes.c_int32)]
 
 
+class CMoeKvConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_q_heads", "n_kv_heads", "head_dim", "n_pages", "max_pages", "max_seqs", "max_rows", "reserved")]
+
+
+class CMoeKvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "page_table", "lens", "score", "pos", "seen")]
+
+
+class CMoeKvBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_rows", "max_q", "reserved")] + [
+        ("row_start", ctypes.c_void_p)]
+
+
 LFU_TABLE_BYTES = ctypes.sizeof(CMoeLfuTable)
 PAIR_BYTES = 16   # MoeFfnPair: blob pointer, int32 inter, int32 token
 TRACE_WORDS = 160  # per CTA trace record of the fused layer kernel
@@ -88,7 +106,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing; build it with "
                           "bit_quantized_expert_int8_b200.build.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    P, i32 = ctypes.c_void_p, ctypes.c_int
+    P, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     sig = {
         "moe_ctx_create": ([ctypes.POINTER(CMoeConfig), i32, ctypes.POINTER(P)], i32),
         "moe_ctx_destroy": ([P], i32),
@@ -118,6 +136,14 @@ def load() -> ctypes.CDLL:
         "moe_store_read": ([P, i32, P, i32, P], i32),
         "moe_store_stats": ([P, ctypes.POINTER(ctypes.c_ulonglong), ctypes.POINTER(ctypes.c_double),
                              ctypes.POINTER(ctypes.c_int)], i32),
+        "moe_kv_page_bytes": ([i32, i32], ctypes.c_size_t),
+        "moe_kv_create": ([ctypes.POINTER(CMoeKvConfig), ctypes.POINTER(P)], i32),
+        "moe_kv_destroy": ([P], i32),
+        "moe_kv_check": ([P, P], i32),
+        "moe_kv_append_q4": ([P, P, P, P, i64, P, i64, P], i32),
+        "moe_kv_read_q4": ([P, P, P, P, i64, P, i64, P], i32),
+        "moe_attn_q4": ([P, P, P, P, i64, ctypes.c_float, i32, i32, P, i64, P, P], i32),
+        "moe_kv_evict": ([P, P, i32, i32, i32, P, P], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -378,3 +404,136 @@ def write_expert_file(path, layers_experts, blob_bytes):
             for e in range(a.shape[0]):
                 f.write(a[e].tobytes())
                 f.write(pad.tobytes())
+
+
+def kv_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    """moe_kv_page_bytes: bytes of one page of the 4-bit KV cache."""
+    return int(load().moe_kv_page_bytes(n_kv_heads, head_dim))
+
+
+class Kv:
+    """moe_kv_create / moe_kv_destroy: context of the 4-bit KV cache calls."""
+
+    def __init__(self, cfg: KvConfig):
+        self.handle = None
+        self.cfg = cfg
+        c = CMoeKvConfig(cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.n_pages, cfg.max_pages,
+                         cfg.max_seqs, cfg.max_rows, 0)
+        h = ctypes.c_void_p()
+        _check(load().moe_kv_create(ctypes.byref(c), ctypes.byref(h)))
+        self.handle = h.value
+
+    def close(self):
+        if self.handle:
+            load().moe_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _need(t, name, dtype, min_numel):
+    """A contiguous tensor of the given type that holds at least min_numel."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < min_numel:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} with at least {min_numel} elements")
+
+
+class KvCache:
+    """The caller's cache buffers as the C MoeKvCache struct (which it keeps
+    alive): pages (n_pages * moe_kv_page_bytes bytes, any type), page_table int32
+    [n_seqs][max_pages], lens int32 [n_seqs]; score fp32 and pos int32
+    [n_seqs][n_kv_heads][64 max_pages] and seen int32 [n_seqs] or None."""
+
+    def __init__(self, kv: Kv, pages, page_table, lens, score=None, pos=None, seen=None):
+        c = kv.cfg
+        n = lens.numel()
+        if not pages.is_contiguous() or \
+                pages.numel() * pages.element_size() < c.n_pages * kv_page_bytes(c.n_kv_heads, c.head_dim):
+            raise MoeError(MOE_ERR_INVALID_ARG, "pages must be contiguous and hold n_pages pages")
+        _need(lens, "lens", torch.int32, 0)
+        _need(page_table, "page_table", torch.int32, n * c.max_pages)
+        per = n * c.n_kv_heads * c.max_pages * MOE_KV_PAGE
+        for t, name, dt, k in ((score, "score", torch.float32, per), (pos, "pos", torch.int32, per),
+                               (seen, "seen", torch.int32, n)):
+            if t is not None:
+                _need(t, name, dt, k)
+        self.n_seqs = n
+        self.keep = (pages, page_table, lens, score, pos, seen)
+        self.c = CMoeKvCache(*[_ptr(t) for t in self.keep])
+        self.ref = ctypes.addressof(self.c)
+
+
+class KvBatch:
+    """One call's rows as the C MoeKvBatch struct: row_start int32 [n_seqs + 1]
+    (device), the rows of the row arrays and the most rows of one sequence."""
+
+    def __init__(self, kv: Kv, row_start, n_rows: int, max_q: int):
+        _need(row_start, "row_start", torch.int32, 1)
+        self.n_seqs = row_start.numel() - 1
+        self.n_rows = int(n_rows)
+        self.keep = row_start
+        self.c = CMoeKvBatch(self.n_seqs, self.n_rows, int(max_q), 0, row_start.data_ptr())
+        self.ref = ctypes.addressof(self.c)
+
+
+def _rows(t, name, batch, heads, dim):
+    """Row stride of an fp16 [n_rows][heads][dim] tensor whose heads are contiguous."""
+    if t.dtype != torch.float16 or t.dim() != 3 or t.shape[0] < batch.n_rows or t.shape[1] != heads or \
+            t.shape[2] != dim or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{name} must be fp16 [n_rows >= {batch.n_rows}][{heads}][{dim}] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _seqs(cache, n_seqs):
+    if n_seqs > cache.n_seqs:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{n_seqs} sequences in a cache of {cache.n_seqs}")
+
+
+def moe_kv_check(kv, stream=None):
+    """Synchronise and raise MoeError if a kernel of this context met a length,
+    row start or page index outside its limits since the last check."""
+    _check(load().moe_kv_check(kv.handle, _stream(stream)))
+
+
+def moe_kv_append_q4(kv, cache: KvCache, batch: KvBatch, k, v, stream=None):
+    c = kv.cfg
+    _seqs(cache, batch.n_seqs)
+    _check(load().moe_kv_append_q4(kv.handle, cache.ref, batch.ref,
+                                   k.data_ptr(), _rows(k, "k", batch, c.n_kv_heads, c.head_dim),
+                                   v.data_ptr(), _rows(v, "v", batch, c.n_kv_heads, c.head_dim),
+                                   _stream(stream)))
+
+
+def moe_kv_read_q4(kv, cache: KvCache, batch: KvBatch, k, v, stream=None):
+    c = kv.cfg
+    _seqs(cache, batch.n_seqs)
+    _check(load().moe_kv_read_q4(kv.handle, cache.ref, batch.ref,
+                                 k.data_ptr(), _rows(k, "k", batch, c.n_kv_heads, c.head_dim),
+                                 v.data_ptr(), _rows(v, "v", batch, c.n_kv_heads, c.head_dim),
+                                 _stream(stream)))
+
+
+def moe_attn_q4(kv, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=1.0, window=0,
+                weights=False, stream=None):
+    """Attention of the batch's rows; weights=True also adds the weight that each
+    entry received to the cache's scores (MOE_ATTN_WEIGHTS)."""
+    c = kv.cfg
+    _seqs(cache, batch.n_seqs)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, batch.n_rows * c.n_q_heads)
+    _check(load().moe_attn_q4(kv.handle, cache.ref, batch.ref,
+                              q.data_ptr(), _rows(q, "q", batch, c.n_q_heads, c.head_dim), scale, window,
+                              MOE_ATTN_WEIGHTS if weights else 0,
+                              out.data_ptr(), _rows(out, "out", batch, c.n_q_heads, c.head_dim),
+                              _ptr(lse), _stream(stream)))
+
+
+def moe_kv_evict(kv, cache: KvCache, n_seqs, budget, n_recent, new_lens, stream=None):
+    _seqs(cache, n_seqs)
+    _need(new_lens, "new_lens", torch.int32, n_seqs)
+    _check(load().moe_kv_evict(kv.handle, cache.ref, n_seqs, budget, n_recent, new_lens.data_ptr(),
+                               _stream(stream)))

@@ -26,8 +26,9 @@
  *  - Pointers marked "device" are CUDA device pointers on the current device;
  *    "host" pointers are ordinary or pinned host memory as stated.
  *  - The caller owns all buffers and streams.  The library allocates only in
- *    moe_ctx_create (workspace, events, mapped host buffers) and frees them in
- *    moe_ctx_destroy; no entry point allocates on the hot path.
+ *    moe_ctx_create (workspace, events, mapped host buffers) and moe_kv_create
+ *    (workspace) and frees in moe_ctx_destroy and moe_kv_destroy; no entry point
+ *    allocates on the hot path.
  *  - Calls are asynchronous on the given stream, except where a host wait is
  *    stated.  One context serves one stream order at a time: calls on the
  *    same context must not overlap on the GPU (they share its workspace).
@@ -487,6 +488,154 @@ int moe_store_stats(const moe_store *store, unsigned long long *bytes,
  *   y_last  device fp32 [T][H] or NULL: MoE output of the last layer */
 int moe_stack_decode(moe_ctx *ctx, const MoeLayer *layers, int n_layers,
                      moe_half *h, int T, float *y_last, moe_stream_t stream);
+
+/* ------------------------------------------------- KV cache in 4 bits ----
+ * The attention side of a decode step.  In the engine of the pages each layer
+ * attends over a bounded fp16 cache of keys and values before its experts run
+ * ([LH] 04 "Le pipeline de traitement"); here the cache is held in the
+ * library's 4-bit affine format (groups of 64 columns, one fp16 scale and
+ * bias, value = scale * code + bias), and an eviction by attention weight
+ * bounds it.  The format of the pages and both rules are this library's.
+ *
+ * Pool and pages.  The caller owns a pool of n_pages pages; a page holds
+ * MOE_KV_PAGE = 64 entries of every kv head.  With NG = head_dim / 64 a page
+ * is [n_kv_heads] tiles of 4608 NG bytes, each
+ *   K codes  u8   [NG][64 entries][32]     column c of the group in nibble
+ *                                          c % 8 of its u32 word c / 8
+ *   K scale, bias fp16 [NG][64 entries][2]
+ *   V codes, V scale and bias in the same order.
+ * Entry j of sequence s is entry j % 64 of page page_table[s][j / 64].  Only
+ * the pages below lens[s] are looked up; sequences may share pages that
+ * nothing writes.
+ *
+ * lens[s] counts the entries that sequence s holds INCLUDING the rows of the
+ * call: the caller advances it before append and attention.  The n rows of
+ * sequence s in a call are rows row_start[s] .. row_start[s + 1] - 1 of the
+ * row arrays (row_start is non-decreasing, its last value at most n_rows);
+ * its row i stands at entry lens[s] - n + i.  Rows that belong to no
+ * sequence are left as they were.
+ *
+ * lens, row_start, page_table and seen live in device memory and are read by
+ * the kernels, so no call waits for the host and every call can be captured
+ * in a CUDA graph.  What they say is checked there: a length outside
+ * 0 .. 64 max_pages is clamped, a sequence whose row_start values decrease,
+ * pass n_rows or give more than max_q rows is skipped, an entry whose page
+ * index is outside 0 .. n_pages - 1 is not read or written; moe_kv_check then
+ * reports MOE_ERR_INVALID_ARG.
+ *
+ * A moe_kv is a context: it belongs to the device that was current when it was
+ * created (calls with another device current are refused) and serves one
+ * stream order at a time; graphs that use the same moe_kv count as such
+ * calls.  Row strides are in elements and multiples of 8; heads are
+ * contiguous within a row ([heads][head_dim]), so K and V may be parts of one
+ * projection's rows.  n_rows = 0 or n_seqs = 0 does nothing. */
+enum { MOE_KV_PAGE = 64 };
+
+typedef struct {
+    int32_t n_q_heads;    /* a multiple of n_kv_heads, at most 1024 */
+    int32_t n_kv_heads;   /* 1..128 */
+    int32_t head_dim;     /* 64, 128, 192 or 256 */
+    int32_t n_pages;      /* pages in the pool */
+    int32_t max_pages;    /* row length of page_table: 1..32768 */
+    int32_t max_seqs;     /* sequences per call: 1..4096 */
+    int32_t max_rows;     /* rows per call: 1..1048576 */
+    int32_t reserved;     /* zero */
+} MoeKvConfig;
+
+typedef struct moe_kv moe_kv;
+
+typedef struct {
+    void *pages;                /* device pool, n_pages * moe_kv_page_bytes */
+    const int32_t *page_table;  /* device [n_seqs][max_pages] */
+    const int32_t *lens;        /* device [n_seqs] */
+    float *score;               /* device [n_seqs][n_kv_heads][64 max_pages] or
+                                   NULL: weight each entry has received */
+    int32_t *pos;               /* device, same shape, or NULL: position of the
+                                   entry's token in its sequence */
+    const int32_t *seen;        /* device [n_seqs], required with pos: tokens the
+                                   sequence has had, the call's rows included
+                                   (lens plus what was evicted) */
+} MoeKvCache;
+
+typedef struct {
+    int32_t n_seqs;
+    int32_t n_rows;             /* rows of the row arrays */
+    int32_t max_q;              /* most rows of one sequence (>= 1) */
+    int32_t reserved;           /* zero */
+    const int32_t *row_start;   /* device [n_seqs + 1] */
+} MoeKvBatch;
+
+/* Bytes of one page; 0 for a shape outside the limits above. */
+size_t moe_kv_page_bytes(int n_kv_heads, int head_dim);
+
+/* Creates a context on the current device.  Allocates the workspace of the
+ * attention calls and a status word; no other call allocates. */
+int moe_kv_create(const MoeKvConfig *cfg, moe_kv **out);
+
+/* Synchronises the device and frees the context.  NULL accepted. */
+int moe_kv_destroy(moe_kv *kv);
+
+/* Synchronises `stream`; MOE_ERR_INVALID_ARG if a kernel of this context met
+ * a length, row start or page index outside its limits since the last check. */
+int moe_kv_check(moe_kv *kv, moe_stream_t stream);
+
+/* Quantises the call's new rows into their entries: per row, kv head and
+ * group of 64 columns, scale = fp16((max - min) / 15), bias = fp16(min),
+ * code = clamp(round-half-even((v - bias) / scale), 0, 15) in fp32 (scale 0:
+ * code 0).  A group that holds an infinity or NaN is stored as NaN (scale and
+ * bias NaN, codes 0).  With cache->score the new entries' scores become 0;
+ * with cache->pos their positions become seen[s] - n + i.
+ *   k, v  device fp16 [n_rows][n_kv_heads][head_dim], 16-byte aligned
+ * A row whose entry would be negative (lens[s] < n) is skipped and reported by
+ * moe_kv_check. */
+int moe_kv_append_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch,
+                     const moe_half *k, int64_t k_stride, const moe_half *v, int64_t v_stride,
+                     moe_stream_t stream);
+
+/* The inverse: the entries of the call's rows as fp16(scale * code + bias)
+ * (formed in fp32).  Same arguments as the append that wrote them. */
+int moe_kv_read_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch,
+                   moe_half *k, int64_t k_stride, moe_half *v, int64_t v_stride,
+                   moe_stream_t stream);
+
+/* Attention of the call's rows over their sequences' entries.  Query head a
+ * reads kv head a / (n_q_heads / n_kv_heads).  A row at entry p sees the
+ * entries j <= p and, when window > 0, j > p - window:
+ *   S_j = scale * (q . k_j),  lse = log sum_j exp(S_j),
+ *   out = sum_j exp(S_j - lse) v_j.
+ * A row that sees nothing (lens[s] < n) gets out = 0 and lse = -infinity.
+ * Entries outside a row's range never touch its result, whatever their pages
+ * hold.
+ *   q    device fp16 [n_rows][n_q_heads][head_dim], out likewise
+ *   lse  device fp32 [n_rows][n_q_heads] or NULL
+ * flags & MOE_ATTN_WEIGHTS: also adds to cache->score, for every entry j and
+ * kv head, sum exp(S_j - lse) over the sequence's rows and the kv head's query
+ * heads (each score is written once, in a fixed order: repeated runs agree bit
+ * for bit). */
+enum { MOE_ATTN_WEIGHTS = 1 };
+
+int moe_attn_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch, const moe_half *q,
+                int64_t q_stride, float scale, int window, int flags, moe_half *out,
+                int64_t out_stride, float *lse, moe_stream_t stream);
+
+/* Bounds every sequence's cache to `budget` entries per kv head by the weight
+ * the entries have received (the expert cache above evicts the least used
+ * expert; this evicts the least attended entry).  For each sequence with
+ * lens[s] > budget and each kv head, `budget` entries stay: those of the last
+ * n_recent tokens (pos >= seen[s] - n_recent) before all others, then by
+ * descending score, ties to the lower index; a NaN score ranks last.  The
+ * entries that stay at an index >= budget move, in index order, into the
+ * places below budget that became free, in index order, with their score and
+ * pos; all other entries stay where they are, and what lies at or behind
+ * budget keeps its bytes.  So at most lens[s] - budget entries move, and the
+ * order of entries is no longer the order of tokens.  (Attention needs no
+ * order, and the rows of the next call still stand behind all others; a
+ * window then counts entries, not tokens.)
+ *   new_lens device int32 [n_seqs] = min(lens[s], budget); must not overlap lens
+ * Needs score, pos and seen, 1 <= budget, 0 <= n_recent <= budget and
+ * max_pages <= 8192. */
+int moe_kv_evict(moe_kv *kv, const MoeKvCache *cache, int n_seqs, int budget, int n_recent,
+                 int32_t *new_lens, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
