@@ -50,7 +50,29 @@ struct moe_kv {
     uint8_t* ws = nullptr;
     int* status = nullptr;
     float* lse = nullptr;      // [max_rows][n_q_heads], where the caller wants none
+    float* part = nullptr;     // partial sums of the split attention
+    int* count = nullptr;      // arrivals per cut item, zero between calls
+    int split_ctas[2] = {0, 0};  // CTAs of the split kernel: 8-row and 16-row tiles
 };
+
+// The split kernel of one head size and row-tile count.
+typedef void (*SplitFn)(const SplitArgs);
+struct SplitKernel {
+    SplitFn fn;
+    int smem, part_floats;
+};
+template <int NG, int RT>
+static SplitKernel split_of() {
+    using Sh = SplitShape<NG, RT>;
+    return {k_attn_split<NG, RT>, Sh::kSmem, Sh::kRows * (Sh::kD + 2)};
+}
+static SplitKernel split_kernel(int ng, int rt) {
+    static const SplitKernel table[4][2] = {{split_of<1, 1>(), split_of<1, 2>()},
+                                            {split_of<2, 1>(), split_of<2, 2>()},
+                                            {split_of<3, 1>(), split_of<3, 2>()},
+                                            {split_of<4, 1>(), split_of<4, 2>()}};
+    return table[ng - 1][rt - 1];
+}
 
 static int kv_check_cfg(const MoeKvConfig* c) {
     if (!c) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_create: cfg is NULL");
@@ -103,9 +125,23 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     auto take = [&](size_t bytes) { const size_t o = off; off = (off + bytes + 255) / 256 * 256; return o; };
     const size_t o_status = take(sizeof(int));
     const size_t o_lse = take((size_t)cfg->max_rows * cfg->n_q_heads * sizeof(float));
+    // every kernel's shared memory limit is raised here: no later call changes it
+    size_t part = 0, ctas = 0;
+    for (int rt = 1; rt <= 2 && e == cudaSuccess; rt++) {
+        const SplitKernel k = split_kernel(cfg->head_dim / 64, rt);
+        int occ = 0;
+        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, kSplitThreads, k.smem);
+        if (e == cudaSuccess && occ < 1) e = cudaErrorInvalidConfiguration;
+        const size_t n = (size_t)kv->n_sms * (occ > 0 ? occ : 1);
+        kv->split_ctas[rt - 1] = (int)n;
+        if (2 * n * k.part_floats > part) part = 2 * n * k.part_floats;
+        if (n > ctas) ctas = n;
+    }
+    const size_t o_part = take(part * sizeof(float));
+    const size_t o_count = take(ctas * sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
     if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
-    // every kernel's shared memory limit is raised here: no later call changes it
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
     if (e != cudaSuccess) {
         const int rc = kv_fail(MOE_ERR_CUDA, "moe_kv_create: %s", cudaGetErrorString(e));
@@ -114,6 +150,8 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     }
     kv->status = reinterpret_cast<int*>(kv->ws + o_status);
     kv->lse = reinterpret_cast<float*>(kv->ws + o_lse);
+    kv->part = reinterpret_cast<float*>(kv->ws + o_part);
+    kv->count = reinterpret_cast<int*>(kv->ws + o_count);
     *out = kv;
     return MOE_OK;
 }
@@ -245,7 +283,14 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     a.out_stride = out_stride;
     a.scale = scale;
     a.window = window;
-    k_attn_simple<<<dim3(batch->n_rows, a.c.hq), 256, 0, stream>>>(a);
+    SplitArgs x{};
+    x.a = a;
+    x.part = kv->part;
+    x.count = kv->count;
+    x.max_rows_seq = 1 << 30;
+    const int rt = a.c.max_q * (a.c.hq / a.c.hkv) <= 8 ? 1 : 2;
+    const SplitKernel k = split_kernel(a.c.ng, rt);
+    k.fn<<<kv->split_ctas[rt - 1], kSplitThreads, k.smem, stream>>>(x);
     KV_CK(cudaGetLastError());
     if (flags & MOE_ATTN_WEIGHTS) {
         k_attn_weights_simple<<<dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream>>>(a);
