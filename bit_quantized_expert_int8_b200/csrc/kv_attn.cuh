@@ -25,27 +25,39 @@ __device__ __forceinline__ float exp2_fast(float x) {       // 2^x, 2 ulp; 0 for
     return y;
 }
 
-// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16); lane = 4 g + t holds
+// D = C + A B on 16 x 8 fp32 (A 16 x 16, B 16 x 8, fp16); lane = 4 g + t holds
 // A rows g (a0, a2) and g + 8 (a1, a3), columns 2t, 2t + 1 (a0, a1) and 8 more
-// (a2, a3); B column g, rows alike; D rows g (c0, c1) and g + 8, columns 2t, 2t + 1.
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+// (a2, a3); B column g, rows alike; C and D rows g (0, 1) and g + 8 (2, 3),
+// columns 2t, 2t + 1.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
-// Nibbles i and i + 4 of w as the fp16 pair (64 + code, 64 + code'): the code
-// lands in mantissa bits 4..7 of 64, so one shift and one masked or serve two
-// codes and no subtraction is needed.  The constant 64 leaves the sums through
-// the bias: s c + b = s (64 + c) + (b - 64 s).  64 rather than 1024 (code in the
-// lowest bits) keeps the cancelling part of the fp32 sums 16 times smaller.
-template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    const uint32_t v = I == 0 ? w << 4 : I == 1 ? w : I == 2 ? w >> 4 : w >> 8;
-    return (v & 0x00F000F0u) | 0x54005400u;
+// Nibbles i and i + 4 of w as the fp16 pair (64 + code, 64 + code'), for i =
+// 0..3.  In mantissa bits 4..7 of 64 a code counts as itself, so nibbles 1 and 3
+// need a masked or; in bits 0..3 of 1024 likewise, and an exact addition of
+// -960 brings 1024 + code to 64 + code (it runs on the half-precision pipe, which
+// has room, instead of a shift on the integer pipe, which has none).  The constant
+// 64 leaves the sums through the bias: s c + b = s (64 + c) + (b - 64 s); 1024 in
+// its place would make the cancelling part of the fp32 sums 16 times larger.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&o)[4]) {
+    const __half2 off = __halves2half2(__ushort_as_half(0xE380), __ushort_as_half(0xE380));   // -960
+    const uint32_t u = w >> 8;
+    const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (u & 0x000F000Fu) | 0x64006400u;
+    const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&b), off);
+    o[0] = *reinterpret_cast<const uint32_t*>(&x);
+    o[1] = (w & 0x00F000F0u) | 0x54005400u;
+    o[2] = *reinterpret_cast<const uint32_t*>(&y);
+    o[3] = (u & 0x00F000F0u) | 0x54005400u;
 }
 constexpr float kCodeOff = 64.f;
 
@@ -75,33 +87,41 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // (row, query head) pairs that read the kv head, so a group's query heads share
 // each entry.  The pages of all items form one list of units; CTA c takes units
 // [c per, (c + 1) per), whatever items they belong to, so ragged batches are
-// even.  Eight warps: warps 0-3 take the four 16-entry parts of even pages of a
-// segment, warps 4-7 of odd ones, each through its own ring of cp.async stages
-// with no barrier between warps.  Per 16 entries a warp forms
-//   S = sum_g s_g (q_g . (64 + c_g)) + (b_g - 64 s_g) sum(q_g)
-// with tensor-core products of the raw codes (m16n8k16, rows = query rows,
-// columns = entries), keeps a running maximum (moved only when it grows by
-// more than 2^8: the sums are rescaled rarely) and adds
-//   O += sum_j p_j s_jg (64 + c_j),   B_g += sum_j p_j (b_jg - 64 s_jg)
-// where p s enters as two fp16 parts (hi, lo: 22 bits; with 8 rows the lower
-// half of the 16-row tile carries lo).  p s is kept in fp16's range by a power
-// of two per warp (vs), raised or lowered when needed.  The warps' sums meet in
-// shared memory; an item cut by CTA borders goes through partial sums in the
-// workspace, joined in a fixed order by the last CTA to arrive (one counter per
-// item start, reset by that CTA).
-constexpr int kSplitWarps = 8;
+// even; an item counts kSplitItemCost pages more than it has, for its start and
+// end.  Four warps: two take the halves of every second page of a segment, each
+// through its own ring of cp.async stages with no barrier between warps.  Per 32
+// entries a warp forms
+//   S = sum_g s_g (q_g . (64 + c_g) - 64 sum(q_g)) + b_g sum(q_g)
+// with tensor-core products of the raw codes (m16n8k16: rows = query rows,
+// columns = entries; the accumulator starts at -64 sum(q_g)), keeps a running
+// maximum (moved only when it grows by more than 2^8, so the sums are rescaled
+// rarely) and adds
+//   O += sum_j p_j s_jg (64 + c_j),   B_g += sum_j p_j (b_jg - 64 s_jg).
+// These products are taken transposed (rows = columns of V, columns = query
+// rows): the scores' registers are then the second operand as they stand, and 8
+// query rows fill a tile.  p s enters as two fp16 parts (hi, lo: 22 bits), kept
+// in fp16's range by a power of two per warp (vs) that is chosen at the first
+// entries and lowered when a later p s would leave the range.  The warps' sums
+// meet in shared memory; an item cut by CTA borders goes through partial sums in
+// the workspace, joined in a fixed order by the last CTA to arrive (one counter
+// per item start, reset by that CTA).
+constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitStages = 4;
+constexpr int kSplitStages = 3;
 constexpr int kSplitMinUnits = 4;      // pages per CTA at least: fewer partial sums in small calls
+constexpr int kSplitItemCost = 2;
 
 template <int NG, int RT>
 struct SplitShape {
     static constexpr int kRows = 8 * RT;
     static constexpr int kD = 64 * NG;
-    static constexpr int kBlock = 1152 * NG;                         // 16 entries: K and V, codes and s, b
-    static constexpr int kRing = kSplitWarps * kSplitStages * kBlock;
-    static constexpr int kJoin = kSplitWarps * kRows * kD * 4;       // the warps' sums, over the ring
-    static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin);
+    static constexpr int kHalf = 2304 * NG;                          // 32 entries: K and V, codes and s, b
+    static constexpr int kRing = kSplitWarps * kSplitStages * kHalf;
+    static constexpr int kJoinRow = kD + 4;                          // floats; 4 more against bank conflicts
+    static constexpr int kJoin = kSplitWarps * kRows * kJoinRow * 4; // the warps' sums, over the ring
+    static constexpr int kQ = NG * 4 * 32 * 8 * RT;                  // query fragments
+    static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
+    static constexpr int kCtas = NG * RT <= 2 ? 4 : 2;               // per SM
 };
 
 struct SplitArgs {
@@ -113,7 +133,7 @@ struct SplitArgs {
 
 // What one sequence asks of the split kernel.
 struct SplitSeq {
-    int n, first, len, plo, np, tiles, units;
+    int n, first, len, plo, np, tiles, units;     // np pages an item
 };
 template <int ROWS>
 __device__ __forceinline__ SplitSeq split_seq(const SplitArgs& x, int s, bool report) {
@@ -126,61 +146,272 @@ __device__ __forceinline__ SplitSeq split_seq(const SplitArgs& x, int s, bool re
     q.plo = lo / kKvPage;
     q.np = max(1, (q.len + kKvPage - 1) / kKvPage - q.plo);
     q.tiles = rows > x.max_rows_seq ? 0 : (rows + ROWS - 1) / ROWS;
-    q.units = q.tiles * c.hkv * q.np;
+    q.units = q.tiles * c.hkv * (q.np + kSplitItemCost);
     return q;
 }
 
+// A warp's running sums of one segment.  Lane (g, t) holds, of group gg and rows
+// 8 z + 2t (even k) and 8 z + 2t + 1 (odd k), columns 8 g + jj (k < 2) and
+// 8 g + 4 + jj in O[z][4 gg + jj][k]; B, m and l belong to row 8 z + g.
 template <int NG, int RT>
-__global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_split(const SplitArgs x) {
+struct SplitAcc {
+    float O[RT][NG * 4][4];
+    float B[NG][RT], m[RT], l[RT];
+    float vs;                  // O is in units of 1 / vs; 0: not chosen
+};
+
+// The value that row 2t (k = 0) or 2t + 1 (k = 1) of a warp has, from row g's.
+__device__ __forceinline__ float row_value(float v, int k) {
+    return __shfl_sync(0xffffffffu, v, 8 * (threadIdx.x & 3) + 4 * k);
+}
+
+// 32 entries (kb: their K block, V block behind it) from entry j0 on.  EDGE:
+// some row does not see some of them.
+template <int NG, int RT, bool EDGE>
+__device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, uint32_t qb, const float (&qs)[NG][RT],
+                                            float sl2, int j0, const int (&pos)[RT], const int (&low)[RT]) {
+    const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+    const uint32_t vb = kb + 1152 * NG;
+    float p[RT][8];
+#pragma unroll
+    for (int z = 0; z < RT; z++)
+#pragma unroll
+        for (int k = 0; k < 8; k++) p[z][k] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+        uint32_t qa[4][4];
+#pragma unroll
+        for (int mm = 0; mm < 4; mm++) {
+            if (RT == 1) {
+                const uint2 v = lds64(qb + ((g * 4 + mm) * 32 + lane) * 8);
+                qa[mm][0] = v.x; qa[mm][2] = v.y; qa[mm][1] = 0; qa[mm][3] = 0;
+            } else {
+                const uint4 v = lds128(qb + ((g * 4 + mm) * 32 + lane) * 16);
+                qa[mm][0] = v.x; qa[mm][1] = v.y; qa[mm][2] = v.z; qa[mm][3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 4; nt++) {
+            const uint2 kw = lds64(kb + g * 1024 + (8 * nt + g8) * 32 + t4 * 8);
+            uint32_t b0[4], b1[4];
+            code_pairs(kw.x, b0);
+            code_pairs(kw.y, b1);
+            const float n0 = -kCodeOff * qs[g][0], n1 = RT == 2 ? -kCodeOff * qs[g][RT - 1] : 0.f;
+            float d[4];
+            mma_f16(d, qa[0][0], qa[0][1], qa[0][2], qa[0][3], b0[0], b1[0], n0, n0, n1, n1);
+            mma_f16(d, qa[1][0], qa[1][1], qa[1][2], qa[1][3], b0[1], b1[1]);
+            mma_f16(d, qa[2][0], qa[2][1], qa[2][2], qa[2][3], b0[2], b1[2]);
+            mma_f16(d, qa[3][0], qa[3][1], qa[3][2], qa[3][3], b0[3], b1[3]);
+            const uint2 sb = lds64(kb + 1024 * NG + g * 128 + (8 * nt + 2 * t4) * 4);
+            const float2 f0 = h2f(sb.x), f1 = h2f(sb.y);
+#pragma unroll
+            for (int z = 0; z < RT; z++) {
+                p[z][2 * nt] = fmaf(f0.x, d[2 * z], fmaf(f0.y, qs[g][z], p[z][2 * nt]));
+                p[z][2 * nt + 1] = fmaf(f1.x, d[2 * z + 1], fmaf(f1.y, qs[g][z], p[z][2 * nt + 1]));
+            }
+        }
+    }
+    // this lane's entries: j0 + 8 (k / 2) + 2 t4 + k % 2
+    unsigned vis[RT];
+    bool grow = false;
+    float top[RT];
+#pragma unroll
+    for (int z = 0; z < RT; z++) {
+        vis[z] = 0xFFu;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            p[z][k] *= sl2;
+            if (EDGE) {
+                const int j = j0 + 8 * (k >> 1) + 2 * t4 + (k & 1);
+                if (j > pos[z] || j < low[z]) {
+                    vis[z] &= ~(1u << k);
+                    p[z][k] = -INFINITY;
+                }
+            }
+        }
+        top[z] = fmaxf(fmaxf(fmaxf(p[z][0], p[z][1]), fmaxf(p[z][2], p[z][3])),
+                       fmaxf(fmaxf(p[z][4], p[z][5]), fmaxf(p[z][6], p[z][7])));
+        top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
+        top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 2));
+        grow = grow || top[z] > A.m[z] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int z = 0; z < RT; z++) {
+            const float m2 = fmaxf(A.m[z], top[z]);
+            const float f = m2 == -INFINITY ? 1.f : exp2_fast(A.m[z] - m2);
+            A.m[z] = m2;
+            A.l[z] *= f;
+            const float f0 = row_value(f, 0), f1 = row_value(f, 1);
+#pragma unroll
+            for (int g = 0; g < NG; g++) A.B[g][z] *= f;
+#pragma unroll
+            for (int j = 0; j < NG * 4; j++) {
+                A.O[z][j][0] *= f0;
+                A.O[z][j][1] *= f1;
+                A.O[z][j][2] *= f0;
+                A.O[z][j][3] *= f1;
+            }
+        }
+    }
+#pragma unroll
+    for (int z = 0; z < RT; z++) {
+        const float ref = A.m[z] == -INFINITY ? 0.f : A.m[z];
+#pragma unroll
+        for (int k = 0; k < 8; k++) p[z][k] = exp2_fast(p[z][k] - ref);
+        A.l[z] += ((p[z][0] + p[z][1]) + (p[z][2] + p[z][3])) + ((p[z][4] + p[z][5]) + (p[z][6] + p[z][7]));
+    }
+    // the weighted sum, 16 entries at a time
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+        uint32_t sb[NG][4], hi[NG][RT][2], lo[NG][RT][2];
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+            const uint2 s0 = lds64(vb + 1024 * NG + g * 128 + b * 64 + t4 * 8);
+            const uint2 s1 = lds64(vb + 1024 * NG + g * 128 + b * 64 + 32 + t4 * 8);
+            sb[g][0] = s0.x; sb[g][1] = s0.y; sb[g][2] = s1.x; sb[g][3] = s1.y;
+        }
+        const auto seen = [&](int z, int k) { return !EDGE || ((vis[z] >> (4 * b + k)) & 1u); };
+        // p s of every group, and whether all of them fit (up to 2^15)
+        const auto parts = [&]() {
+            __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+            for (int g = 0; g < NG; g++)
+#pragma unroll
+                for (int z = 0; z < RT; z++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const float2 f0 = h2f(sb[g][2 * k]), f1 = h2f(sb[g][2 * k + 1]);
+                        // an entry out of sight may hold a NaN scale
+                        const float e0 = seen(z, 2 * k) ? p[z][4 * b + 2 * k] * A.vs * f0.x : 0.f;
+                        const float e1 = seen(z, 2 * k + 1) ? p[z][4 * b + 2 * k + 1] * A.vs * f1.x : 0.f;
+                        hi[g][z][k] = f2h(e0, e1);
+                        const float2 r = h2f(hi[g][z][k]);
+                        lo[g][z][k] = f2h(e0 - r.x, e1 - r.y);
+                        big = __hmax2(big, __habs2(*reinterpret_cast<const __half2*>(&hi[g][z][k])));
+                    }
+            return fmaxf(__low2float(big), __high2float(big)) <= 32768.f;
+        };
+        const bool fits = parts();
+        if (__any_sync(0xffffffffu, !fits || A.vs == 0.f)) {
+            // the unit becomes the power of two that brings the largest p s to 16..32
+            float mx = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; g++)
+#pragma unroll
+                for (int z = 0; z < RT; z++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (seen(z, k)) mx = fmaxf(mx, fabsf(p[z][4 * b + k] * h2f(sb[g][k]).x));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (mx > 0.f && mx < 1e30f) {                // else nothing here, or nothing finite to keep
+                const float v2 = exp2f(fminf(4.f - floorf(log2f(mx)), 100.f));
+                const float f = A.vs == 0.f ? 1.f : v2 / A.vs;
+                A.vs = v2;
+#pragma unroll
+                for (int z = 0; z < RT; z++)
+#pragma unroll
+                    for (int j = 0; j < NG * 4; j++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) A.O[z][j][k] *= f;
+            } else if (A.vs == 0.f && !(mx == 0.f)) {
+                A.vs = 1.f;
+            }
+            parts();
+        }
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = h2f(sb[g][k]);
+                const float o = fmaf(-kCodeOff, f.x, f.y);
+#pragma unroll
+                for (int z = 0; z < RT; z++)
+                    if (seen(z, k)) A.B[g][z] = fmaf(p[z][4 * b + k], o, A.B[g][z]);
+            }
+            const uint32_t va = vb + g * 1024 + b * 512 + t4 * 32 + g8 * 4;
+            const uint32_t w0 = lds32(va), w1 = lds32(va + 128), w2 = lds32(va + 256), w3 = lds32(va + 384);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            code_pairs(__byte_perm(w0, w1, 0x5410), a0);
+            code_pairs(__byte_perm(w0, w1, 0x7632), a1);
+            code_pairs(__byte_perm(w2, w3, 0x5410), a2);
+            code_pairs(__byte_perm(w2, w3, 0x7632), a3);
+#pragma unroll
+            for (int jj = 0; jj < 4; jj++)
+#pragma unroll
+                for (int z = 0; z < RT; z++) {
+                    float(&o)[4] = A.O[z][g * 4 + jj];
+                    mma_f16(o, a0[jj], a1[jj], a2[jj], a3[jj], hi[g][z][0], hi[g][z][1]);
+                    mma_f16(o, a0[jj], a1[jj], a2[jj], a3[jj], lo[g][z][0], lo[g][z][1]);
+                }
+        }
+    }
+}
+
+template <int NG, int RT>
+__global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_attn_split(const SplitArgs x) {
     using Sh = SplitShape<NG, RT>;
-    constexpr int R = Sh::kRows, D = Sh::kD;
+    constexpr int R = Sh::kRows, D = Sh::kD, JR = Sh::kJoinRow;
     extern __shared__ __align__(128) uint8_t sp_smem[];
-    __shared__ float s_m[kSplitWarps][R], s_l[kSplitWarps][R];
-    __shared__ int s_last;
+    __shared__ float s_m[kSplitWarps][R], s_l[kSplitWarps][R], s_qs[NG][R];
+    __shared__ long long s_plan[2];
+    __shared__ int s_seq, s_last;
     const AttnArgs& a = x.a;
     const KvArgs& c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int G = c.hq / c.hkv;
-    const int cap_pages = c.max_pages;
+    uint8_t* q_smem = sp_smem + Sh::kSmem - Sh::kQ;
 
-    // units of all sequences, then this CTA's range
-    long long total = 0;
-    for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-        const int s = s0 + lane;
-        total += s < c.n_seqs ? split_seq<R>(x, s, blockIdx.x == 0 && warp == 0).units : 0;
+    // units of all sequences, this CTA's range and the sequence it begins in
+    if (warp == 0) {
+        long long total = 0;
+        for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
+            const int s = s0 + lane;
+            total += s < c.n_seqs ? split_seq<R>(x, s, blockIdx.x == 0).units : 0;
+        }
+        total = warp_sum(total);
+        const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kSplitMinUnits);
+        const long long u = blockIdx.x * per;
+        int s = 0;
+        long long base = 0;
+        if (u < total)
+            for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
+                const int sl = s0 + lane;
+                const int w = sl < c.n_seqs ? split_seq<R>(x, sl, false).units : 0;
+                long long inc = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
+                if (hit) {
+                    const int at = __ffs(hit) - 1;
+                    s = s0 + at;
+                    base += __shfl_sync(0xffffffffu, inc - w, at);
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        if (lane == 0) {
+            s_plan[0] = total;
+            s_plan[1] = base;
+            s_seq = s;
+        }
     }
-    total = warp_sum(total);
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kSplitMinUnits) per = kSplitMinUnits;
-    long long u = blockIdx.x * per;
+    __syncthreads();
+    const long long total = s_plan[0];
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kSplitMinUnits);
+    long long u = blockIdx.x * per, s_base = s_plan[1];
     const long long u_end = min(total, u + per);
     if (u >= u_end) return;
-
-    // sequence that holds unit u, and the units before it
-    int s = 0;
-    long long s_base = 0;
-    for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-        const int sl = s0 + lane;
-        const int w = sl < c.n_seqs ? split_seq<R>(x, sl, false).units : 0;
-        long long inc = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, s_base + inc > u);
-        if (hit) {
-            const int at = __ffs(hit) - 1;
-            s = s0 + at;
-            s_base += __shfl_sync(0xffffffffu, inc - w, at);
-            break;
-        }
-        s_base += __shfl_sync(0xffffffffu, inc, 31);
-    }
+    int s = s_seq;
     SplitSeq q = split_seq<R>(x, s, false);
 
-    const uint32_t ring = smem_u32(sp_smem) + warp * (kSplitStages * Sh::kBlock);
-    const int sub = warp & 3, par = warp >> 2;
+    const uint32_t ring = smem_u32(sp_smem) + warp * (kSplitStages * Sh::kHalf);
+    const int half = warp & 1, par = warp >> 1;
+    constexpr int kStep = kSplitWarps / 2;                   // pages a round
     const float sl2 = a.scale * kLog2e;
 
     while (u < u_end) {
@@ -189,291 +420,145 @@ __global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_sp
             s++;
             q = split_seq<R>(x, s, false);
         }
-        const int item = (int)((u - s_base) / q.np);
-        const long long ib = s_base + (long long)item * q.np, ie = ib + q.np;
+        const int item = (int)(u - s_base) / (q.np + kSplitItemCost);
+        // the item's pages stand at units ib .. ie - 1, behind its fixed cost
+        const long long ib = s_base + (long long)item * (q.np + kSplitItemCost) + kSplitItemCost, ie = ib + q.np;
+        u = max(u, ib);
+        if (u >= u_end) break;
         const int rt = item / c.hkv, h = item % c.hkv;
         const int pg0 = q.plo + (int)(u - ib);
-        const int pg1 = q.plo + (int)(min(u_end, ie) - ib);
         const int pend = (q.len + kKvPage - 1) / kKvPage;    // pages that hold entries
+        const int pg1 = min(q.plo + (int)(min(u_end, ie) - ib), pend);
         const int p0 = q.len - q.n;
         const int rows = q.n * G;
         u = min(u_end, ie);
 
-        // queries of this tile: row g8 (and g8 + 8) of the 16-row operand
-        uint32_t qa[NG][4][2 * RT];
-        float qs[NG][RT];
-        int pos[RT], low[RT];
-#pragma unroll
-        for (int z = 0; z < RT; z++) {
-            const int r = rt * R + g8 + 8 * z, rr = min(r, rows - 1);
-            const int i = rr / G, head = h * G + rr % G;
-            const __half* qp = a.q + (size_t)(q.first + i) * a.q_stride + (size_t)head * D;
-            pos[z] = p0 + i;
-            low[z] = a.window > 0 ? p0 + i - a.window + 1 : 0;
-#pragma unroll
-            for (int g = 0; g < NG; g++) {
-                uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-                if (r < rows) {
-                    v0 = *reinterpret_cast<const uint4*>(qp + g * 64 + t4 * 16);
-                    v1 = *reinterpret_cast<const uint4*>(qp + g * 64 + t4 * 16 + 8);
-                }
-                // columns (m, m + 4) of each 8, as the code pairs come
-                qa[g][0][z] = __byte_perm(v0.x, v0.z, 0x5410);
-                qa[g][1][z] = __byte_perm(v0.x, v0.z, 0x7632);
-                qa[g][2][z] = __byte_perm(v0.y, v0.w, 0x5410);
-                qa[g][3][z] = __byte_perm(v0.y, v0.w, 0x7632);
-                qa[g][0][RT + z] = __byte_perm(v1.x, v1.z, 0x5410);
-                qa[g][1][RT + z] = __byte_perm(v1.x, v1.z, 0x7632);
-                qa[g][2][RT + z] = __byte_perm(v1.y, v1.w, 0x5410);
-                qa[g][3][RT + z] = __byte_perm(v1.y, v1.w, 0x7632);
-                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const float2 f = h2f(w[k]);
-                    sum += f.x + f.y;
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                qs[g][z] = sum;
-            }
-        }
-        const int first_pos = p0 + (rt * R) / G;             // least and greatest row of the tile
-        const int last_low = a.window > 0 ? p0 + (min(rt * R + R, rows) - 1) / G - a.window + 1 : 0;
-
-        float O[NG * 8][4];
-        float B[NG][RT], m[RT], l[RT];
-        float vs = 1.f, top_ps = 0.f;                        // unit not chosen yet: any p s is above it
-#pragma unroll
-        for (int j = 0; j < NG * 8; j++)
-#pragma unroll
-            for (int k = 0; k < 4; k++) O[j][k] = 0.f;
-#pragma unroll
-        for (int z = 0; z < RT; z++) {
-            m[z] = -INFINITY;
-            l[z] = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; g++) B[g][z] = 0.f;
-        }
-
-        // stage k of this warp holds its 16 entries of page pg0 + par + 2 k
+        // the stage holds this warp's half of page pg0 + par + kStep k
         unsigned ok = 0;                                     // bit: the stage's page is usable
-        const int32_t* trow = c.table + (size_t)s * cap_pages;
+        const int32_t* trow = c.table + (size_t)s * c.max_pages;
+        int id = pg0 + par < pg1 ? trow[pg0 + par] : -1;     // page of the next fetch, read one ahead
         const auto fetch = [&](int pg, int st) {
             ok &= ~(1u << st);
-            if (pg < pg1 && pg < pend) {
-                const int id = trow[pg];
+            if (pg < pg1) {
                 if ((unsigned)id < (unsigned)c.n_pages) {
                     ok |= 1u << st;
-                    const uint8_t* src = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG);
-                    const uint32_t dst = ring + st * Sh::kBlock;
+                    const uint8_t* src = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG) + half * 1024;
+                    const uint32_t dst = ring + st * Sh::kHalf;
                     const int e = lane >> 1;                 // V rows: entries 2t, 2t + 1, 8 more as rows t, 4 + t
                     const int vr = (e & 8) + ((e & 1) << 2) + ((e & 7) >> 1);
 #pragma unroll
-                    for (int g = 0; g < NG; g++) {
-                        cp_async16(dst + g * 512 + lane * 16, src + g * 2048 + sub * 512 + lane * 16);
-                        cp_async16(dst + 576 * NG + g * 512 + vr * 32 + (lane & 1) * 16,
-                                   src + 2304 * NG + g * 2048 + sub * 512 + lane * 16);
-                    }
-                    if (lane < 8 * NG) {
-                        const int v = lane / (4 * NG), k = lane % (4 * NG);
-                        cp_async16(dst + v * 576 * NG + 512 * NG + k * 16,
-                                   src + v * 2304 * NG + 2048 * NG + (k >> 2) * 256 + sub * 64 + (k & 3) * 16);
+                    for (int g = 0; g < NG; g++)
+#pragma unroll
+                        for (int b = 0; b < 2; b++) {
+                            cp_async16(dst + g * 1024 + b * 512 + lane * 16, src + g * 2048 + b * 512 + lane * 16);
+                            cp_async16(dst + 1152 * NG + g * 1024 + b * 512 + vr * 32 + (lane & 1) * 16,
+                                       src + 2304 * NG + g * 2048 + b * 512 + lane * 16);
+                        }
+#pragma unroll
+                    for (int k0 = 0; k0 < 16 * NG; k0 += 32) {
+                        const int k = k0 + lane;
+                        if (k < 16 * NG) {
+                            const int v = k / (8 * NG), i = k % (8 * NG);
+                            cp_async16(dst + v * 1152 * NG + 1024 * NG + i * 16,
+                                       src - half * 1024 + v * 2304 * NG + 2048 * NG + (i >> 3) * 256 + half * 128 + (i & 7) * 16);
+                        }
                     }
                 } else if (lane == 0) {
                     kv_flag(c.status);
                 }
+                if (pg + kStep < pg1) id = trow[pg + kStep];
             }
             cp_async_commit();
         };
 #pragma unroll
-        for (int st = 0; st < kSplitStages - 1; st++) fetch(pg0 + par + 2 * st, st);
+        for (int st = 0; st < kSplitStages - 1; st++) fetch(pg0 + par + kStep * st, st);
 
+        // queries of the tile into the operand order of code_pairs: per group, 4 steps of
+        // 16 columns; lane (g8, t4) holds columns 16 t4 + m (+ 4, + 8, + 12) of rows g8, g8 + 8
+        for (int k = tid; k < NG * R * 4; k += kSplitThreads) {
+            const int t = k & 3, r = (k >> 2) % R, g = (k >> 2) / R;
+            uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+            if (rt * R + r < rows) {
+                const int rr = rt * R + r;
+                const __half* qp = a.q + (size_t)(q.first + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + g * 64 + t * 16;
+                v0 = *reinterpret_cast<const uint4*>(qp);
+                v1 = *reinterpret_cast<const uint4*>(qp + 8);
+            }
+            uint32_t* dst = reinterpret_cast<uint32_t*>(q_smem) + ((g * 4) * 32 + (r & 7) * 4 + t) * (2 * RT) + (r >> 3);
+            const uint32_t w0[4] = {__byte_perm(v0.x, v0.z, 0x5410), __byte_perm(v0.x, v0.z, 0x7632),
+                                    __byte_perm(v0.y, v0.w, 0x5410), __byte_perm(v0.y, v0.w, 0x7632)};
+            const uint32_t w1[4] = {__byte_perm(v1.x, v1.z, 0x5410), __byte_perm(v1.x, v1.z, 0x7632),
+                                    __byte_perm(v1.y, v1.w, 0x5410), __byte_perm(v1.y, v1.w, 0x7632)};
+            float sum = 0.f;
+#pragma unroll
+            for (int mm = 0; mm < 4; mm++) {
+                dst[mm * 32 * 2 * RT] = w0[mm];
+                dst[mm * 32 * 2 * RT + RT] = w1[mm];
+                const float2 f0 = h2f(w0[mm]), f1 = h2f(w1[mm]);
+                sum += (f0.x + f0.y) + (f1.x + f1.y);
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);     // NG R 4 is a multiple of 32
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (t == 0) s_qs[g][r] = sum;
+        }
+        __syncthreads();
+
+        float qs[NG][RT];
+        int pos[RT], low[RT];
+#pragma unroll
+        for (int z = 0; z < RT; z++) {
+            pos[z] = p0 + min(rt * R + g8 + 8 * z, rows - 1) / G;
+            low[z] = a.window > 0 ? pos[z] - a.window + 1 : 0;
+#pragma unroll
+            for (int g = 0; g < NG; g++) qs[g][z] = s_qs[g][g8 + 8 * z];
+        }
+        const int first_pos = p0 + (rt * R) / G;             // least and greatest row of the tile
+        const int last_low = a.window > 0 ? p0 + (min(rt * R + R, rows) - 1) / G - a.window + 1 : 0;
+
+        SplitAcc<NG, RT> A;
+        A.vs = 0.f;
+#pragma unroll
+        for (int z = 0; z < RT; z++) {
+            A.m[z] = -INFINITY;
+            A.l[z] = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; g++) A.B[g][z] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NG * 4; j++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) A.O[z][j][k] = 0.f;
+        }
+        const uint32_t qb = smem_u32(q_smem);
         int st = 0;
-        for (int pg = pg0 + par; pg < pg1; pg += 2) {
-            fetch(pg + 2 * (kSplitStages - 1), (st + kSplitStages - 1) % kSplitStages);
+        for (int pg = pg0 + par; pg < pg1; pg += kStep) {
+            fetch(pg + kStep * (kSplitStages - 1), st == 0 ? kSplitStages - 1 : st - 1);
             cp_async_wait<kSplitStages - 1>();
             __syncwarp();
-            const uint32_t kb = ring + st * Sh::kBlock, vb = kb + 576 * NG;
+            const uint32_t kb = ring + st * Sh::kHalf;
             const bool page_ok = (ok >> st) & 1u;
-            st = (st + 1) % kSplitStages;
-            const int j0 = pg * kKvPage + sub * 16;
+            st = st == kSplitStages - 1 ? 0 : st + 1;
+            const int j0 = pg * kKvPage + half * 32;
             if (!page_ok || j0 >= q.len) continue;           // nothing here (all lanes alike)
-
-            float S[2][2 * RT];
-#pragma unroll
-            for (int nt = 0; nt < 2; nt++) {
-#pragma unroll
-                for (int k = 0; k < 2 * RT; k++) S[nt][k] = 0.f;
-#pragma unroll
-                for (int g = 0; g < NG; g++) {
-                    const uint2 kw = lds64(kb + g * 512 + (8 * nt + g8) * 32 + t4 * 8);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    const uint32_t z0 = 0;
-                    mma_f16(d, qa[g][0][0], RT == 2 ? qa[g][0][RT - 1] : z0, qa[g][0][RT], RT == 2 ? qa[g][0][2 * RT - 1] : z0,
-                            code_pair<0>(kw.x), code_pair<0>(kw.y));
-                    mma_f16(d, qa[g][1][0], RT == 2 ? qa[g][1][RT - 1] : z0, qa[g][1][RT], RT == 2 ? qa[g][1][2 * RT - 1] : z0,
-                            code_pair<1>(kw.x), code_pair<1>(kw.y));
-                    mma_f16(d, qa[g][2][0], RT == 2 ? qa[g][2][RT - 1] : z0, qa[g][2][RT], RT == 2 ? qa[g][2][2 * RT - 1] : z0,
-                            code_pair<2>(kw.x), code_pair<2>(kw.y));
-                    mma_f16(d, qa[g][3][0], RT == 2 ? qa[g][3][RT - 1] : z0, qa[g][3][RT], RT == 2 ? qa[g][3][2 * RT - 1] : z0,
-                            code_pair<3>(kw.x), code_pair<3>(kw.y));
-                    const uint2 sb = lds64(kb + 512 * NG + g * 64 + (8 * nt + 2 * t4) * 4);
-                    const float2 f0 = h2f(sb.x), f1 = h2f(sb.y);
-                    const float o0 = fmaf(-kCodeOff, f0.x, f0.y), o1 = fmaf(-kCodeOff, f1.x, f1.y);
-#pragma unroll
-                    for (int z = 0; z < RT; z++) {
-                        S[nt][2 * z] = fmaf(f0.x, d[2 * z], fmaf(o0, qs[g][z], S[nt][2 * z]));
-                        S[nt][2 * z + 1] = fmaf(f1.x, d[2 * z + 1], fmaf(o1, qs[g][z], S[nt][2 * z + 1]));
-                    }
-                }
-            }
-            // entries of this lane: j0 + 2 t4, + 1, + 8, + 9
-            const bool edge = j0 + 15 > first_pos || j0 < last_low;
-            unsigned vis[RT];
-            float p[RT][4];
-            bool grow = false;
-            float top[RT];
-#pragma unroll
-            for (int z = 0; z < RT; z++) {
-                vis[z] = 0xFu;
-                float* pz = p[z];
-                pz[0] = S[0][2 * z] * sl2;
-                pz[1] = S[0][2 * z + 1] * sl2;
-                pz[2] = S[1][2 * z] * sl2;
-                pz[3] = S[1][2 * z + 1] * sl2;
-                if (edge) {
-                    vis[z] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const int j = j0 + 2 * t4 + (k & 1) + 8 * (k >> 1);
-                        if (j <= pos[z] && j >= low[z]) vis[z] |= 1u << k;
-                        else pz[k] = -INFINITY;
-                    }
-                }
-                top[z] = fmaxf(fmaxf(pz[0], pz[1]), fmaxf(pz[2], pz[3]));
-                top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
-                top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 2));
-                grow = grow || top[z] > m[z] + 8.f;
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int z = 0; z < RT; z++) {
-                    const float m2 = fmaxf(m[z], top[z]);
-                    const float f = m2 == -INFINITY ? 1.f : exp2_fast(m[z] - m2);
-                    m[z] = m2;
-                    l[z] *= f;
-#pragma unroll
-                    for (int g = 0; g < NG; g++) B[g][z] *= f;
-#pragma unroll
-                    for (int j = 0; j < NG * 8; j++) {
-                        O[j][2 * z] *= f;
-                        O[j][2 * z + 1] *= f;
-                        if (RT == 1) {
-                            O[j][2] *= f;
-                            O[j][3] *= f;
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int z = 0; z < RT; z++) {
-                const float ref = m[z] == -INFINITY ? 0.f : m[z];
-#pragma unroll
-                for (int k = 0; k < 4; k++) p[z][k] = exp2_fast(p[z][k] - ref);
-                l[z] += (p[z][0] + p[z][1]) + (p[z][2] + p[z][3]);
-            }
-            // the weighted sum, one group of 64 columns at a time
-#pragma unroll
-            for (int g = 0; g < NG; g++) {
-                const uint2 sb0 = lds64(vb + 512 * NG + g * 64 + t4 * 8);
-                const uint2 sb1 = lds64(vb + 512 * NG + g * 64 + 32 + t4 * 8);
-                const float2 f[4] = {h2f(sb0.x), h2f(sb0.y), h2f(sb1.x), h2f(sb1.y)};   // scale, bias
-                float e[RT][4];
-#pragma unroll
-                for (int z = 0; z < RT; z++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        e[z][k] = !edge || ((vis[z] >> k) & 1u) ? p[z][k] * f[k].x : 0.f;
-                uint32_t hi[RT][2], lo[RT][2];
-                float big = 0.f;
-#pragma unroll
-                for (int z = 0; z < RT; z++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) big = fmaxf(big, fabsf(e[z][k]));
-                if (__any_sync(0xffffffffu, big > top_ps)) {
-                    // above fp16's range in the present unit (or the first entries): the unit
-                    // becomes the power of two that brings the largest p s to 16..32
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    if (big < 1e30f) {                       // an infinite scale: nothing finite to keep
-                        const float v2 = exp2f(fminf(4.f - floorf(log2f(big)), 100.f));
-                        const float k = top_ps == 0.f ? 1.f : v2 / vs;
-                        vs = v2;
-                        top_ps = 16384.f / v2;
-#pragma unroll
-                        for (int z = 0; z < RT; z++)
-#pragma unroll
-                            for (int gg = 0; gg < NG; gg++) B[gg][z] *= k;
-#pragma unroll
-                        for (int j = 0; j < NG * 8; j++)
-#pragma unroll
-                            for (int w = 0; w < 4; w++) O[j][w] *= k;
-                    }
-                }
-#pragma unroll
-                for (int z = 0; z < RT; z++) {
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        e[z][k] *= vs;
-                        if (!edge || ((vis[z] >> k) & 1u))
-                            B[g][z] = fmaf(p[z][k] * vs, fmaf(-kCodeOff, f[k].x, f[k].y), B[g][z]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        hi[z][k] = f2h(e[z][2 * k], e[z][2 * k + 1]);
-                        const float2 r = h2f(hi[z][k]);
-                        lo[z][k] = f2h(e[z][2 * k] - r.x, e[z][2 * k + 1] - r.y);
-                    }
-                }
-                const uint32_t va = vb + g * 512 + t4 * 32 + g8 * 4;
-                const uint32_t w0 = lds32(va), w1 = lds32(va + 128), w2 = lds32(va + 256), w3 = lds32(va + 384);
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const uint32_t c0 = __byte_perm(w0, w1, k ? 0x7632 : 0x5410);
-                    const uint32_t c1 = __byte_perm(w2, w3, k ? 0x7632 : 0x5410);
-                    const uint32_t e0[4] = {code_pair<0>(c0), code_pair<1>(c0), code_pair<2>(c0), code_pair<3>(c0)};
-                    const uint32_t e1[4] = {code_pair<0>(c1), code_pair<1>(c1), code_pair<2>(c1), code_pair<3>(c1)};
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        float(&o)[4] = O[g * 8 + k * 4 + j];
-                        if (RT == 1) {
-                            mma_f16(o, hi[0][0], lo[0][0], hi[0][1], lo[0][1], e0[j], e1[j]);
-                        } else {
-                            mma_f16(o, hi[0][0], hi[RT - 1][0], hi[0][1], hi[RT - 1][1], e0[j], e1[j]);
-                            mma_f16(o, lo[0][0], lo[RT - 1][0], lo[0][1], lo[RT - 1][1], e0[j], e1[j]);
-                        }
-                    }
-                }
-            }
+            if (j0 + 31 > first_pos || j0 < last_low) split_block<NG, RT, true>(A, kb, qb, qs, sl2, j0, pos, low);
+            else split_block<NG, RT, false>(A, kb, qb, qs, sl2, j0, pos, low);
             __syncwarp();
         }
         cp_async_wait<0>();
 
         // join the warps: sums to shared memory (over the ring), relative to each warp's maximum
-        const float inv = 1.f / vs;                          // a power of two
+        const float inv = A.vs == 0.f ? 1.f : 1.f / A.vs;    // a power of two
 #pragma unroll
         for (int z = 0; z < RT; z++) {
-            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
-            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
+            A.l[z] += __shfl_xor_sync(0xffffffffu, A.l[z], 1);
+            A.l[z] += __shfl_xor_sync(0xffffffffu, A.l[z], 2);
 #pragma unroll
             for (int g = 0; g < NG; g++) {
-                B[g][z] += __shfl_xor_sync(0xffffffffu, B[g][z], 1);
-                B[g][z] += __shfl_xor_sync(0xffffffffu, B[g][z], 2);
+                A.B[g][z] += __shfl_xor_sync(0xffffffffu, A.B[g][z], 1);
+                A.B[g][z] += __shfl_xor_sync(0xffffffffu, A.B[g][z], 2);
             }
             if (t4 == 0) {
-                s_m[warp][g8 + 8 * z] = m[z];
-                s_l[warp][g8 + 8 * z] = l[z];
+                s_m[warp][g8 + 8 * z] = A.m[z];
+                s_l[warp][g8 + 8 * z] = A.l[z];
             }
         }
         __syncthreads();                                     // every warp has left its ring
@@ -481,15 +566,16 @@ __global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_sp
 #pragma unroll
         for (int z = 0; z < RT; z++)
 #pragma unroll
-            for (int g = 0; g < NG; g++) {
-                float* dst = join + ((size_t)warp * R + g8 + 8 * z) * D + g * 64 + t4 * 16;
+            for (int g = 0; g < NG; g++)
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float(&o)[4] = O[g * 8 + j];
-                    dst[j] = ((RT == 1 ? o[0] + o[2] : o[2 * z]) + B[g][z]) * inv;
-                    dst[8 + j] = ((RT == 1 ? o[1] + o[3] : o[2 * z + 1]) + B[g][z]) * inv;
+                for (int k = 0; k < 2; k++) {                // rows 2t and 2t + 1
+                    const float bb = row_value(A.B[g][z], k);
+                    float4* dst = reinterpret_cast<float4*>(join + ((size_t)warp * R + 8 * z + 2 * t4 + k) * JR + g * 64 + g8 * 8);
+                    const float(*v)[4] = &A.O[z][g * 4];
+                    dst[0] = make_float4(fmaf(v[0][k], inv, bb), fmaf(v[1][k], inv, bb), fmaf(v[2][k], inv, bb), fmaf(v[3][k], inv, bb));
+                    dst[1] = make_float4(fmaf(v[0][2 + k], inv, bb), fmaf(v[1][2 + k], inv, bb), fmaf(v[2][2 + k], inv, bb),
+                                         fmaf(v[3][2 + k], inv, bb));
                 }
-            }
         __syncthreads();
         const bool whole = u == ie && ib >= blockIdx.x * per;
         const int c0 = (int)(ib / per), c1 = (int)((ie - 1) / per);
@@ -505,6 +591,12 @@ __global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_sp
             *reinterpret_cast<uint4*>(a.out + (size_t)(q.first + i) * a.out_stride + (size_t)head * D + d) = v;
             if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         };
+        const auto add = [](float (&o)[8], float f, float4 v0, float4 v1) {
+            o[0] = fmaf(f, v0.x, o[0]); o[1] = fmaf(f, v0.y, o[1]);
+            o[2] = fmaf(f, v0.z, o[2]); o[3] = fmaf(f, v0.w, o[3]);
+            o[4] = fmaf(f, v1.x, o[4]); o[5] = fmaf(f, v1.y, o[5]);
+            o[6] = fmaf(f, v1.z, o[6]); o[7] = fmaf(f, v1.w, o[7]);
+        };
         for (int k = tid; k < R * (D / 8); k += kSplitThreads) {
             const int r = k / (D / 8), d = (k % (D / 8)) * 8;
             if (rt * R + r >= rows) continue;
@@ -514,15 +606,11 @@ __global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_sp
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < kSplitWarps; w++) {
-                if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.f) continue;
+                if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.f) continue;   // the warp's entries are not seen
                 const float f = exp2_fast(s_m[w][r] - ref);
-                const float4* src = reinterpret_cast<const float4*>(join + ((size_t)w * R + r) * D + d);
-                const float4 v0 = src[0], v1 = src[1];
+                const float4* src = reinterpret_cast<const float4*>(join + ((size_t)w * R + r) * JR + d);
                 L = fmaf(f, s_l[w][r], L);
-                o[0] = fmaf(f, v0.x, o[0]); o[1] = fmaf(f, v0.y, o[1]);
-                o[2] = fmaf(f, v0.z, o[2]); o[3] = fmaf(f, v0.w, o[3]);
-                o[4] = fmaf(f, v1.x, o[4]); o[5] = fmaf(f, v1.y, o[5]);
-                o[6] = fmaf(f, v1.z, o[6]); o[7] = fmaf(f, v1.w, o[7]);
+                add(o, f, src[0], src[1]);
             }
             if (whole) {
                 store_row(rt * R + r, d, o, M, L);
@@ -556,13 +644,9 @@ __global__ void __launch_bounds__(kSplitThreads, NG * RT <= 2 ? 2 : 1) k_attn_sp
                         const float mb = __ldcg(src + R * D + r), lb = __ldcg(src + R * D + R + r);
                         const float4 v0 = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + d));
                         const float4 v1 = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + d) + 1);
-                        const bool none = mb == -INFINITY && lb == 0.f;
-                        const float f = none ? 0.f : exp2_fast(mb - ref);
+                        const float f = mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref);
                         L = fmaf(f, lb, L);
-                        o[0] = fmaf(f, v0.x, o[0]); o[1] = fmaf(f, v0.y, o[1]);
-                        o[2] = fmaf(f, v0.z, o[2]); o[3] = fmaf(f, v0.w, o[3]);
-                        o[4] = fmaf(f, v1.x, o[4]); o[5] = fmaf(f, v1.y, o[5]);
-                        o[6] = fmaf(f, v1.z, o[6]); o[7] = fmaf(f, v1.w, o[7]);
+                        add(o, f, v0, v1);
                     }
                     store_row(rt * R + r, d, o, M, L);
                 }
