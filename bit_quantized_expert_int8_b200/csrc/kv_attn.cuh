@@ -41,25 +41,20 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
-// Nibbles i and i + 4 of w as the fp16 pair (64 + code, 64 + code'), for i =
-// 0..3.  In mantissa bits 4..7 of 64 a code counts as itself, so nibbles 1 and 3
-// need a masked or; in bits 0..3 of 1024 likewise, and an exact addition of
-// -960 brings 1024 + code to 64 + code (it runs on the half-precision pipe, which
-// has room, instead of a shift on the integer pipe, which has none).  The constant
-// 64 leaves the sums through the bias: s c + b = s (64 + c) + (b - 64 s); 1024 in
-// its place would make the cancelling part of the fp32 sums 16 times larger.
+// Nibbles i and i + 4 of w as a pair of fp16 operands, i = 0..3.  fp16's
+// subnormals and first binade are linear in their bits, so a code in bits 0..3 is
+// the number code * 2^-24 as it stands and one in bits 4..7 is 16 times that: a
+// mask makes an operand, exactly, with no exponent to set and no offset to take
+// out again.  The factors 2^24 and 16 leave through the query operand (K) or the
+// sums (V).
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&o)[4]) {
-    const __half2 off = __halves2half2(__ushort_as_half(0xE380), __ushort_as_half(0xE380));   // -960
     const uint32_t u = w >> 8;
-    const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (u & 0x000F000Fu) | 0x64006400u;
-    const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&b), off);
-    o[0] = *reinterpret_cast<const uint32_t*>(&x);
-    o[1] = (w & 0x00F000F0u) | 0x54005400u;
-    o[2] = *reinterpret_cast<const uint32_t*>(&y);
-    o[3] = (u & 0x00F000F0u) | 0x54005400u;
+    o[0] = w & 0x000F000Fu;
+    o[1] = w & 0x00F000F0u;
+    o[2] = u & 0x000F000Fu;
+    o[3] = u & 0x00F000F0u;
 }
-constexpr float kCodeOff = 64.f;
+constexpr float kCodeUnit = 16777216.f;       // 2^24: operands of even pairs are code / 2^24, of odd ones 16 times it
 
 __device__ __forceinline__ float2 h2f(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 __device__ __forceinline__ uint32_t f2h(float lo, float hi) {
@@ -91,12 +86,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // end.  Four warps: two take the halves of every second page of a segment, each
 // through its own ring of cp.async stages with no barrier between warps.  Per 32
 // entries a warp forms
-//   S = sum_g s_g (q_g . (64 + c_g) - 64 sum(q_g)) + b_g sum(q_g)
+//   S = sum_g s_g (q_g . c_g) + b_g sum(q_g)
 // with tensor-core products of the raw codes (m16n8k16: rows = query rows,
-// columns = entries; the accumulator starts at -64 sum(q_g)), keeps a running
+// columns = entries; q is taken times a power of two per row that brings its
+// largest to 1024..2048, so that 16 q, for the even pairs, stays exact), keeps a running
 // maximum (moved only when it grows by more than 2^8, so the sums are rescaled
 // rarely) and adds
-//   O += sum_j p_j s_jg (64 + c_j),   B_g += sum_j p_j (b_jg - 64 s_jg).
+//   O += sum_j p_j s_jg c_j,   B_g += sum_j p_j b_jg.
 // These products are taken transposed (rows = columns of V, columns = query
 // rows): the scores' registers are then the second operand as they stand, and 8
 // query rows fill a tile.  p s enters as two fp16 parts (hi, lo: 22 bits), kept
@@ -109,7 +105,7 @@ constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitStages = 3;
 constexpr int kSplitMinUnits = 4;      // pages per CTA at least: fewer partial sums in small calls
-constexpr int kSplitItemCost = 2;
+constexpr int kSplitItemCost = 4;
 
 template <int NG, int RT>
 struct SplitShape {
@@ -121,7 +117,7 @@ struct SplitShape {
     static constexpr int kJoin = kSplitWarps * kRows * kJoinRow * 4; // the warps' sums, over the ring
     static constexpr int kQ = NG * 4 * 32 * 8 * RT;                  // query fragments
     static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
-    static constexpr int kCtas = NG * RT <= 2 ? 4 : 2;               // per SM
+    static constexpr int kCtas = NG * RT <= 2 ? 3 : 2;               // per SM
 };
 
 struct SplitArgs {
@@ -169,7 +165,7 @@ __device__ __forceinline__ float row_value(float v, int k) {
 // some row does not see some of them.
 template <int NG, int RT, bool EDGE>
 __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, uint32_t qb, const float (&qs)[NG][RT],
-                                            float sl2, int j0, const int (&pos)[RT], const int (&low)[RT]) {
+                                            const float (&sl2)[RT], int j0, const int (&pos)[RT], const int (&low)[RT]) {
     const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
     const uint32_t vb = kb + 1152 * NG;
     float p[RT][8];
@@ -196,9 +192,8 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
             uint32_t b0[4], b1[4];
             code_pairs(kw.x, b0);
             code_pairs(kw.y, b1);
-            const float n0 = -kCodeOff * qs[g][0], n1 = RT == 2 ? -kCodeOff * qs[g][RT - 1] : 0.f;
             float d[4];
-            mma_f16(d, qa[0][0], qa[0][1], qa[0][2], qa[0][3], b0[0], b1[0], n0, n0, n1, n1);
+            mma_f16(d, qa[0][0], qa[0][1], qa[0][2], qa[0][3], b0[0], b1[0], 0.f, 0.f, 0.f, 0.f);
             mma_f16(d, qa[1][0], qa[1][1], qa[1][2], qa[1][3], b0[1], b1[1]);
             mma_f16(d, qa[2][0], qa[2][1], qa[2][2], qa[2][3], b0[2], b1[2]);
             mma_f16(d, qa[3][0], qa[3][1], qa[3][2], qa[3][3], b0[3], b1[3]);
@@ -220,7 +215,7 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
         vis[z] = 0xFFu;
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            p[z][k] *= sl2;
+            p[z][k] *= sl2[z];
             if (EDGE) {
                 const int j = j0 + 8 * (k >> 1) + 2 * t4 + (k & 1);
                 if (j > pos[z] || j < low[z]) {
@@ -325,10 +320,9 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const float2 f = h2f(sb[g][k]);
-                const float o = fmaf(-kCodeOff, f.x, f.y);
 #pragma unroll
                 for (int z = 0; z < RT; z++)
-                    if (seen(z, k)) A.B[g][z] = fmaf(p[z][4 * b + k], o, A.B[g][z]);
+                    if (seen(z, k)) A.B[g][z] = fmaf(p[z][4 * b + k], f.y, A.B[g][z]);
             }
             const uint32_t va = vb + g * 1024 + b * 512 + t4 * 32 + g8 * 4;
             const uint32_t w0 = lds32(va), w1 = lds32(va + 128), w2 = lds32(va + 256), w3 = lds32(va + 384);
@@ -338,13 +332,14 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
             code_pairs(__byte_perm(w2, w3, 0x5410), a2);
             code_pairs(__byte_perm(w2, w3, 0x7632), a3);
 #pragma unroll
-            for (int jj = 0; jj < 4; jj++)
+            for (int z = 0; z < RT; z++) {
 #pragma unroll
-                for (int z = 0; z < RT; z++) {
-                    float(&o)[4] = A.O[z][g * 4 + jj];
-                    mma_f16(o, a0[jj], a1[jj], a2[jj], a3[jj], hi[g][z][0], hi[g][z][1]);
-                    mma_f16(o, a0[jj], a1[jj], a2[jj], a3[jj], lo[g][z][0], lo[g][z][1]);
-                }
+                for (int jj = 0; jj < 4; jj++)
+                    mma_f16(A.O[z][g * 4 + jj], a0[jj], a1[jj], a2[jj], a3[jj], hi[g][z][0], hi[g][z][1]);
+#pragma unroll
+                for (int jj = 0; jj < 4; jj++)
+                    mma_f16(A.O[z][g * 4 + jj], a0[jj], a1[jj], a2[jj], a3[jj], lo[g][z][0], lo[g][z][1]);
+            }
         }
     }
 }
@@ -354,7 +349,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     using Sh = SplitShape<NG, RT>;
     constexpr int R = Sh::kRows, D = Sh::kD, JR = Sh::kJoinRow;
     extern __shared__ __align__(128) uint8_t sp_smem[];
-    __shared__ float s_m[kSplitWarps][R], s_l[kSplitWarps][R], s_qs[NG][R];
+    __shared__ float s_m[kSplitWarps][R], s_l[kSplitWarps][R], s_qs[NG][R], s_sl2[R];
     __shared__ long long s_plan[2];
     __shared__ int s_seq, s_last;
     const AttnArgs& a = x.a;
@@ -412,7 +407,6 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     const uint32_t ring = smem_u32(sp_smem) + warp * (kSplitStages * Sh::kHalf);
     const int half = warp & 1, par = warp >> 1;
     constexpr int kStep = kSplitWarps / 2;                   // pages a round
-    const float sl2 = a.scale * kLog2e;
 
     while (u < u_end) {
         while (u >= s_base + q.units) {                      // sequences without units are passed over
@@ -475,40 +469,61 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
 
         // queries of the tile into the operand order of code_pairs: per group, 4 steps of
         // 16 columns; lane (g8, t4) holds columns 16 t4 + m (+ 4, + 8, + 12) of rows g8, g8 + 8
-        for (int k = tid; k < NG * R * 4; k += kSplitThreads) {
-            const int t = k & 3, r = (k >> 2) % R, g = (k >> 2) / R;
-            uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-            if (rt * R + r < rows) {
-                const int rr = rt * R + r;
-                const __half* qp = a.q + (size_t)(q.first + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + g * 64 + t * 16;
-                v0 = *reinterpret_cast<const uint4*>(qp);
-                v1 = *reinterpret_cast<const uint4*>(qp + 8);
-            }
-            uint32_t* dst = reinterpret_cast<uint32_t*>(q_smem) + ((g * 4) * 32 + (r & 7) * 4 + t) * (2 * RT) + (r >> 3);
-            const uint32_t w0[4] = {__byte_perm(v0.x, v0.z, 0x5410), __byte_perm(v0.x, v0.z, 0x7632),
-                                    __byte_perm(v0.y, v0.w, 0x5410), __byte_perm(v0.y, v0.w, 0x7632)};
-            const uint32_t w1[4] = {__byte_perm(v1.x, v1.z, 0x5410), __byte_perm(v1.x, v1.z, 0x7632),
-                                    __byte_perm(v1.y, v1.w, 0x5410), __byte_perm(v1.y, v1.w, 0x7632)};
-            float sum = 0.f;
+        if (tid < R * 4) {
+            const int t = tid & 3, r = tid >> 2;
+            uint4 v[NG][2];
+            float mx = 0.f;
 #pragma unroll
-            for (int mm = 0; mm < 4; mm++) {
-                dst[mm * 32 * 2 * RT] = w0[mm];
-                dst[mm * 32 * 2 * RT + RT] = w1[mm];
-                const float2 f0 = h2f(w0[mm]), f1 = h2f(w1[mm]);
-                sum += (f0.x + f0.y) + (f1.x + f1.y);
+            for (int g = 0; g < NG; g++) {
+                v[g][0] = v[g][1] = make_uint4(0, 0, 0, 0);
+                if (rt * R + r < rows) {
+                    const int rr = rt * R + r;
+                    const __half* qp = a.q + (size_t)(q.first + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + g * 64 + t * 16;
+                    v[g][0] = *reinterpret_cast<const uint4*>(qp);
+                    v[g][1] = *reinterpret_cast<const uint4*>(qp + 8);
+                }
+                const uint32_t w[8] = {v[g][0].x, v[g][0].y, v[g][0].z, v[g][0].w, v[g][1].x, v[g][1].y, v[g][1].z, v[g][1].w};
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float2 f = h2f(w[k]);
+                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);     // NG R 4 is a multiple of 32
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (t == 0) s_qs[g][r] = sum;
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float up = mx > 0.f && mx < 1e30f ? exp2f(10.f - floorf(log2f(mx))) : 1.f;
+            if (t == 0) s_sl2[r] = a.scale * kLog2e * (kCodeUnit / 16.f) / up;
+#pragma unroll
+            for (int g = 0; g < NG; g++) {
+                uint32_t* dst = reinterpret_cast<uint32_t*>(q_smem) + ((g * 4) * 32 + (r & 7) * 4 + t) * (2 * RT) + (r >> 3);
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const uint4 x4 = v[g][e];
+                    const uint32_t w[4] = {__byte_perm(x4.x, x4.z, 0x5410), __byte_perm(x4.x, x4.z, 0x7632),
+                                           __byte_perm(x4.y, x4.w, 0x5410), __byte_perm(x4.y, x4.w, 0x7632)};
+#pragma unroll
+                    for (int mm = 0; mm < 4; mm++) {
+                        const float2 f = h2f(w[mm]);
+                        sum += f.x * up + f.y * up;
+                        const float u16 = mm & 1 ? up : 16.f * up;
+                        dst[mm * 32 * 2 * RT + e * RT] = f2h(f.x * u16, f.y * u16);
+                    }
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (t == 0) s_qs[g][r] = sum * (16.f / kCodeUnit);
+            }
         }
         __syncthreads();
 
-        float qs[NG][RT];
+        float qs[NG][RT], sl2[RT];
         int pos[RT], low[RT];
 #pragma unroll
         for (int z = 0; z < RT; z++) {
             pos[z] = p0 + min(rt * R + g8 + 8 * z, rows - 1) / G;
             low[z] = a.window > 0 ? pos[z] - a.window + 1 : 0;
+            sl2[z] = s_sl2[g8 + 8 * z];
 #pragma unroll
             for (int g = 0; g < NG; g++) qs[g][z] = s_qs[g][g8 + 8 * z];
         }
@@ -546,7 +561,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         cp_async_wait<0>();
 
         // join the warps: sums to shared memory (over the ring), relative to each warp's maximum
-        const float inv = A.vs == 0.f ? 1.f : 1.f / A.vs;    // a power of two
+        const float inv = A.vs == 0.f ? 1.f : kCodeUnit / A.vs, inv16 = inv * 0.0625f;   // powers of two
 #pragma unroll
         for (int z = 0; z < RT; z++) {
             A.l[z] += __shfl_xor_sync(0xffffffffu, A.l[z], 1);
@@ -572,9 +587,9 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                     const float bb = row_value(A.B[g][z], k);
                     float4* dst = reinterpret_cast<float4*>(join + ((size_t)warp * R + 8 * z + 2 * t4 + k) * JR + g * 64 + g8 * 8);
                     const float(*v)[4] = &A.O[z][g * 4];
-                    dst[0] = make_float4(fmaf(v[0][k], inv, bb), fmaf(v[1][k], inv, bb), fmaf(v[2][k], inv, bb), fmaf(v[3][k], inv, bb));
-                    dst[1] = make_float4(fmaf(v[0][2 + k], inv, bb), fmaf(v[1][2 + k], inv, bb), fmaf(v[2][2 + k], inv, bb),
-                                         fmaf(v[3][2 + k], inv, bb));
+                    dst[0] = make_float4(fmaf(v[0][k], inv, bb), fmaf(v[1][k], inv16, bb), fmaf(v[2][k], inv, bb), fmaf(v[3][k], inv16, bb));
+                    dst[1] = make_float4(fmaf(v[0][2 + k], inv, bb), fmaf(v[1][2 + k], inv16, bb), fmaf(v[2][2 + k], inv, bb),
+                                         fmaf(v[3][2 + k], inv16, bb));
                 }
         __syncthreads();
         const bool whole = u == ie && ib >= blockIdx.x * per;
