@@ -42,6 +42,23 @@ static int kv_fail(int code, const char* fmt, ...) {
 
 static inline bool kv_al(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Launch that may be scheduled before the kernel ahead of it in the stream ends
+// (every kernel here begins with kv_begin, which waits for it).
+template <typename... P, typename... A>
+static cudaError_t kv_launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, fn, static_cast<P>(args)...);
+}
+
 struct moe_kv {
     MoeKvConfig cfg{};
     int device = 0;
@@ -239,9 +256,8 @@ static int kv_rows_call(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* b
     const KvArgs a = kv_args(kv, cache, batch, batch->n_seqs);
     __half* kp = reinterpret_cast<__half*>(k);
     __half* vp = reinterpret_cast<__half*>(v);
-    if (read) k_kv_rows<true><<<batch->n_rows, kKvRowThreads, 0, s>>>(a, kp, k_stride, vp, v_stride);
-    else k_kv_rows<false><<<batch->n_rows, kKvRowThreads, 0, s>>>(a, kp, k_stride, vp, v_stride);
-    KV_CK(cudaGetLastError());
+    KV_CK(kv_launch(read ? k_kv_rows<true> : k_kv_rows<false>, dim3(batch->n_rows), kKvRowThreads, 0, s, a, kp,
+                    k_stride, vp, v_stride));
     return MOE_OK;
 }
 
@@ -290,12 +306,9 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     x.max_rows_seq = 1 << 30;
     const int rt = a.c.max_q * (a.c.hq / a.c.hkv) <= 8 ? 1 : 2;
     const SplitKernel k = split_kernel(a.c.ng, rt);
-    k.fn<<<kv->split_ctas[rt - 1], kSplitThreads, k.smem, stream>>>(x);
-    KV_CK(cudaGetLastError());
-    if (flags & MOE_ATTN_WEIGHTS) {
-        k_attn_weights_simple<<<dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream>>>(a);
-        KV_CK(cudaGetLastError());
-    }
+    KV_CK(kv_launch(k.fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads, k.smem, stream, x));
+    if (flags & MOE_ATTN_WEIGHTS)
+        KV_CK(kv_launch(k_attn_weights_simple, dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream, a));
     return MOE_OK;
 }
 
@@ -318,7 +331,6 @@ extern "C" int moe_kv_evict(moe_kv* kv, const MoeKvCache* cache, int n_seqs, int
         return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: max_pages=%d above 8192", who, kv->cfg.max_pages);
     KV_TRY(kv_check_device(kv, who));
     const KvArgs a = kv_args(kv, cache, nullptr, n_seqs);
-    k_kv_evict<<<dim3(a.hkv, n_seqs), kEvictThreads, smem, stream>>>(a, budget, n_recent, new_lens);
-    KV_CK(cudaGetLastError());
+    KV_CK(kv_launch(k_kv_evict, dim3(a.hkv, n_seqs), kEvictThreads, smem, stream, a, budget, n_recent, new_lens));
     return MOE_OK;
 }

@@ -1,7 +1,6 @@
 // kv_attn.cuh -- attention over the 4-bit KV cache.
 #pragma once
 #include "kv_cache.cuh"
-#include "ptx.cuh"
 
 namespace moeq4 {
 
@@ -96,8 +95,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // These products are taken transposed (rows = columns of V, columns = query
 // rows): the scores' registers are then the second operand as they stand, and 8
 // query rows fill a tile.  p s enters as two fp16 parts (hi, lo: 22 bits), kept
-// in fp16's range by a power of two per warp (vs) that is chosen at the first
-// entries and lowered when a later p s would leave the range.  The warps' sums
+// in fp16's range by a power of two per warp (unit) that is chosen at the first
+// entries and lowered when a later p s would leave the range; it is part of the
+// exponent that p is formed with.  The warps' sums
 // meet in shared memory; an item cut by CTA borders goes through partial sums in
 // the workspace, joined in a fixed order by the last CTA to arrive (one counter
 // per item start, reset by that CTA).
@@ -115,7 +115,7 @@ struct SplitShape {
     static constexpr int kRing = kSplitWarps * kSplitStages * kHalf;
     static constexpr int kJoinRow = kD + 4;                          // floats; 4 more against bank conflicts
     static constexpr int kJoin = kSplitWarps * kRows * kJoinRow * 4; // the warps' sums, over the ring
-    static constexpr int kQ = NG * 4 * 32 * 8 * RT;                  // query fragments
+    static constexpr int kQ = NG * 4 * 32 * 16;                      // query operand, 16 rows (zeros behind 8)
     static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
     static constexpr int kCtas = NG * RT <= 2 ? 3 : 2;               // per SM
 };
@@ -153,7 +153,8 @@ template <int NG, int RT>
 struct SplitAcc {
     float O[RT][NG * 4][4];
     float B[NG][RT], m[RT], l[RT];
-    float vs;                  // O is in units of 1 / vs; 0: not chosen
+    float unit;                // all sums are taken times 2^unit
+    bool chosen;
 };
 
 // The value that row 2t (k = 0) or 2t + 1 (k = 1) of a warp has, from row g's.
@@ -178,13 +179,8 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
         uint32_t qa[4][4];
 #pragma unroll
         for (int mm = 0; mm < 4; mm++) {
-            if (RT == 1) {
-                const uint2 v = lds64(qb + ((g * 4 + mm) * 32 + lane) * 8);
-                qa[mm][0] = v.x; qa[mm][2] = v.y; qa[mm][1] = 0; qa[mm][3] = 0;
-            } else {
-                const uint4 v = lds128(qb + ((g * 4 + mm) * 32 + lane) * 16);
-                qa[mm][0] = v.x; qa[mm][1] = v.y; qa[mm][2] = v.z; qa[mm][3] = v.w;
-            }
+            const uint4 v = lds128(qb + ((g * 4 + mm) * 32 + lane) * 16);
+            qa[mm][0] = v.x; qa[mm][1] = v.y; qa[mm][2] = v.z; qa[mm][3] = v.w;
         }
 #pragma unroll
         for (int nt = 0; nt < 4; nt++) {
@@ -214,20 +210,18 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
     for (int z = 0; z < RT; z++) {
         vis[z] = 0xFFu;
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            p[z][k] *= sl2[z];
-            if (EDGE) {
-                const int j = j0 + 8 * (k >> 1) + 2 * t4 + (k & 1);
-                if (j > pos[z] || j < low[z]) {
-                    vis[z] &= ~(1u << k);
-                    p[z][k] = -INFINITY;
-                }
+        for (int k = 0; EDGE && k < 8; k++) {
+            const int j = j0 + 8 * (k >> 1) + 2 * t4 + (k & 1);
+            if (j > pos[z] || j < low[z]) {
+                vis[z] &= ~(1u << k);
+                p[z][k] = -INFINITY;
             }
         }
         top[z] = fmaxf(fmaxf(fmaxf(p[z][0], p[z][1]), fmaxf(p[z][2], p[z][3])),
                        fmaxf(fmaxf(p[z][4], p[z][5]), fmaxf(p[z][6], p[z][7])));
         top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
         top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 2));
+        top[z] *= sl2[z];                                    // sl2 > 0
         grow = grow || top[z] > A.m[z] + 8.f;
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -251,9 +245,9 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
     }
 #pragma unroll
     for (int z = 0; z < RT; z++) {
-        const float ref = A.m[z] == -INFINITY ? 0.f : A.m[z];
+        const float ref = A.m[z] == -INFINITY ? 0.f : A.m[z] - A.unit;
 #pragma unroll
-        for (int k = 0; k < 8; k++) p[z][k] = exp2_fast(p[z][k] - ref);
+        for (int k = 0; k < 8; k++) p[z][k] = exp2_fast(fmaf(p[z][k], sl2[z], -ref));
         A.l[z] += ((p[z][0] + p[z][1]) + (p[z][2] + p[z][3])) + ((p[z][4] + p[z][5]) + (p[z][6] + p[z][7]));
     }
     // the weighted sum, 16 entries at a time
@@ -278,8 +272,8 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
                     for (int k = 0; k < 2; k++) {
                         const float2 f0 = h2f(sb[g][2 * k]), f1 = h2f(sb[g][2 * k + 1]);
                         // an entry out of sight may hold a NaN scale
-                        const float e0 = seen(z, 2 * k) ? p[z][4 * b + 2 * k] * A.vs * f0.x : 0.f;
-                        const float e1 = seen(z, 2 * k + 1) ? p[z][4 * b + 2 * k + 1] * A.vs * f1.x : 0.f;
+                        const float e0 = seen(z, 2 * k) ? p[z][4 * b + 2 * k] * f0.x : 0.f;
+                        const float e1 = seen(z, 2 * k + 1) ? p[z][4 * b + 2 * k + 1] * f1.x : 0.f;
                         hi[g][z][k] = f2h(e0, e1);
                         const float2 r = h2f(hi[g][z][k]);
                         lo[g][z][k] = f2h(e0 - r.x, e1 - r.y);
@@ -288,8 +282,8 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
             return fmaxf(__low2float(big), __high2float(big)) <= 32768.f;
         };
         const bool fits = parts();
-        if (__any_sync(0xffffffffu, !fits || A.vs == 0.f)) {
-            // the unit becomes the power of two that brings the largest p s to 16..32
+        if (__any_sync(0xffffffffu, !fits || !A.chosen)) {
+            // the unit becomes the one that brings the largest p s to 16..32
             float mx = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; g++)
@@ -301,19 +295,24 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (mx > 0.f && mx < 1e30f) {                // else nothing here, or nothing finite to keep
-                const float v2 = exp2f(fminf(4.f - floorf(log2f(mx)), 100.f));
-                const float f = A.vs == 0.f ? 1.f : v2 / A.vs;
-                A.vs = v2;
+                const float du = fmaxf(fminf(4.f - floorf(log2f(mx)), 60.f - A.unit), -60.f - A.unit);
+                const float f = exp2f(du);
+                A.unit += du;
+                A.chosen = true;
 #pragma unroll
-                for (int z = 0; z < RT; z++)
+                for (int z = 0; z < RT; z++) {
+                    A.l[z] *= f;
+#pragma unroll
+                    for (int g = 0; g < NG; g++) A.B[g][z] *= f;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) p[z][k] *= f;
 #pragma unroll
                     for (int j = 0; j < NG * 4; j++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) A.O[z][j][k] *= f;
-            } else if (A.vs == 0.f && !(mx == 0.f)) {
-                A.vs = 1.f;
+                }
+                parts();
             }
-            parts();
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) {
@@ -358,6 +357,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     const int G = c.hq / c.hkv;
     uint8_t* q_smem = sp_smem + Sh::kSmem - Sh::kQ;
 
+    kv_begin();
     // units of all sequences, this CTA's range and the sequence it begins in
     if (warp == 0) {
         long long total = 0;
@@ -407,6 +407,20 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     const uint32_t ring = smem_u32(sp_smem) + warp * (kSplitStages * Sh::kHalf);
     const int half = warp & 1, par = warp >> 1;
     constexpr int kStep = kSplitWarps / 2;                   // pages a round
+    // this lane's parts of a fetch: codes of V go to rows in the order that the products
+    // want (entries 2t, 2t + 1, 8 + 2t, 9 + 2t as rows t, 4 + t, 8 + t, 12 + t); scales and
+    // biases, 16 bytes each
+    const size_t page_bytes = (size_t)c.hkv * (4608 * NG);
+    const int ve = lane >> 1;
+    const uint32_t v_dst = 1152 * NG + ((ve & 8) + ((ve & 1) << 2) + ((ve & 7) >> 1)) * 32 + (lane & 1) * 16;
+    uint32_t sb_dst[(NG + 1) / 2];
+    int sb_src[(NG + 1) / 2];
+#pragma unroll
+    for (int k = 0; k < (NG + 1) / 2; k++) {
+        const int n = k * 32 + lane, v = n / (8 * NG), i = n % (8 * NG);
+        sb_dst[k] = v * 1152 * NG + 1024 * NG + i * 16;
+        sb_src[k] = v * 2304 * NG + 2048 * NG + (i >> 3) * 256 + half * 128 + (i & 7) * 16 - half * 1024 - lane * 16;
+    }
 
     while (u < u_end) {
         while (u >= s_base + q.units) {                      // sequences without units are passed over
@@ -431,32 +445,24 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         unsigned ok = 0;                                     // bit: the stage's page is usable
         const int32_t* trow = c.table + (size_t)s * c.max_pages;
         int id = pg0 + par < pg1 ? trow[pg0 + par] : -1;     // page of the next fetch, read one ahead
+        const uint8_t* pool = c.pages + (size_t)h * (4608 * NG) + half * 1024 + lane * 16;
         const auto fetch = [&](int pg, int st) {
             ok &= ~(1u << st);
             if (pg < pg1) {
                 if ((unsigned)id < (unsigned)c.n_pages) {
                     ok |= 1u << st;
-                    const uint8_t* src = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG) + half * 1024;
+                    const uint8_t* src = pool + (size_t)id * page_bytes;
                     const uint32_t dst = ring + st * Sh::kHalf;
-                    const int e = lane >> 1;                 // V rows: entries 2t, 2t + 1, 8 more as rows t, 4 + t
-                    const int vr = (e & 8) + ((e & 1) << 2) + ((e & 7) >> 1);
 #pragma unroll
                     for (int g = 0; g < NG; g++)
 #pragma unroll
                         for (int b = 0; b < 2; b++) {
-                            cp_async16(dst + g * 1024 + b * 512 + lane * 16, src + g * 2048 + b * 512 + lane * 16);
-                            cp_async16(dst + 1152 * NG + g * 1024 + b * 512 + vr * 32 + (lane & 1) * 16,
-                                       src + 2304 * NG + g * 2048 + b * 512 + lane * 16);
+                            cp_async16(dst + lane * 16 + g * 1024 + b * 512, src + g * 2048 + b * 512);
+                            cp_async16(dst + v_dst + g * 1024 + b * 512, src + 2304 * NG + g * 2048 + b * 512);
                         }
 #pragma unroll
-                    for (int k0 = 0; k0 < 16 * NG; k0 += 32) {
-                        const int k = k0 + lane;
-                        if (k < 16 * NG) {
-                            const int v = k / (8 * NG), i = k % (8 * NG);
-                            cp_async16(dst + v * 1152 * NG + 1024 * NG + i * 16,
-                                       src - half * 1024 + v * 2304 * NG + 2048 * NG + (i >> 3) * 256 + half * 128 + (i & 7) * 16);
-                        }
-                    }
+                    for (int k = 0; k < (NG + 1) / 2; k++)
+                        if (k * 32 + lane < 16 * NG) cp_async16(dst + sb_dst[k], src + sb_src[k]);
                 } else if (lane == 0) {
                     kv_flag(c.status);
                 }
@@ -491,11 +497,13 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float up = mx > 0.f && mx < 1e30f ? exp2f(10.f - floorf(log2f(mx))) : 1.f;
-            if (t == 0) s_sl2[r] = a.scale * kLog2e * (kCodeUnit / 16.f) / up;
+            // the sign of the softmax scale goes into the query: maxima are then taken of S itself
+            const float mag = mx > 0.f && mx < 1e30f ? exp2f(10.f - floorf(log2f(mx))) : 1.f;
+            const float up = a.scale > 0.f ? mag : a.scale < 0.f ? -mag : 0.f;
+            if (t == 0) s_sl2[r] = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e * (kCodeUnit / 16.f) / mag;
 #pragma unroll
             for (int g = 0; g < NG; g++) {
-                uint32_t* dst = reinterpret_cast<uint32_t*>(q_smem) + ((g * 4) * 32 + (r & 7) * 4 + t) * (2 * RT) + (r >> 3);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(q_smem) + ((g * 4) * 32 + (r & 7) * 4 + t) * 4 + (r >> 3);
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
@@ -507,7 +515,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                         const float2 f = h2f(w[mm]);
                         sum += f.x * up + f.y * up;
                         const float u16 = mm & 1 ? up : 16.f * up;
-                        dst[mm * 32 * 2 * RT + e * RT] = f2h(f.x * u16, f.y * u16);
+                        dst[mm * 128 + e * 2] = f2h(f.x * u16, f.y * u16);
+                        if (RT == 1) dst[mm * 128 + e * 2 + 1] = 0;
                     }
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -531,7 +540,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         const int last_low = a.window > 0 ? p0 + (min(rt * R + R, rows) - 1) / G - a.window + 1 : 0;
 
         SplitAcc<NG, RT> A;
-        A.vs = 0.f;
+        A.unit = 0.f;
+        A.chosen = false;
 #pragma unroll
         for (int z = 0; z < RT; z++) {
             A.m[z] = -INFINITY;
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         cp_async_wait<0>();
 
         // join the warps: sums to shared memory (over the ring), relative to each warp's maximum
-        const float inv = A.vs == 0.f ? 1.f : kCodeUnit / A.vs, inv16 = inv * 0.0625f;   // powers of two
+        constexpr float inv = kCodeUnit, inv16 = kCodeUnit / 16.f;
 #pragma unroll
         for (int z = 0; z < RT; z++) {
             A.l[z] += __shfl_xor_sync(0xffffffffu, A.l[z], 1);
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                 A.B[g][z] += __shfl_xor_sync(0xffffffffu, A.B[g][z], 2);
             }
             if (t4 == 0) {
-                s_m[warp][g8 + 8 * z] = A.m[z];
+                s_m[warp][g8 + 8 * z] = A.m[z] == -INFINITY ? A.m[z] : A.m[z] - A.unit;
                 s_l[warp][g8 + 8 * z] = A.l[z];
             }
         }
@@ -685,6 +695,7 @@ __device__ __forceinline__ float kv_value(const uint8_t* tile, const KvTile& t, 
 __global__ void __launch_bounds__(kKvPage) k_attn_weights_simple(const AttnArgs a) {
     const KvArgs& c = a.c;
     const int pg = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
+    kv_begin();
     const int len = kv_len(c, s, false), j = pg * kKvPage + tid;
     int first;
     const int n = kv_rows(c, s, &first, false);

@@ -2,6 +2,7 @@
 // eviction by accumulated attention weight.  Layout and rules in moeq4.h.
 #pragma once
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace moeq4 {
 
@@ -29,6 +30,13 @@ struct KvArgs {
     int* status;
     int n_seqs, n_rows, max_q, hq, hkv, ng, n_pages, max_pages;
 };
+
+// The kernels of a decode step follow one another closely: each lets the next
+// be scheduled early and waits here for the work before it, so launches overlap.
+__device__ __forceinline__ void kv_begin() {
+    griddep_launch_dependents();
+    griddep_wait();
+}
 
 __device__ __forceinline__ void kv_flag(int* status) { atomicCAS(status, 0, MOE_ERR_INVALID_ARG); }
 
@@ -78,6 +86,7 @@ template <bool READ>
 __global__ void __launch_bounds__(kKvRowThreads)
 k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_stride) {
     const int r = blockIdx.x;
+    kv_begin();
     const int s = kv_seq_of_row(a, r);
     if (s >= a.n_seqs) return;                                  // behind the last sequence
     int first;
@@ -224,6 +233,7 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
     extern __shared__ __align__(16) uint32_t ev_smem[];
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
     const int cap = a.max_pages * kKvPage;
+    kv_begin();
     const int len = kv_len(a, s, h == 0 && tid == 0);
     if (h == 0 && tid == 0) new_lens[s] = min(len, budget);
     if (len <= budget) return;

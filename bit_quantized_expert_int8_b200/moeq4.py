@@ -437,7 +437,7 @@ class Kv:
 
 def _need(t, name, dtype, min_numel):
     """A contiguous tensor of the given type that holds at least min_numel."""
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < min_numel:
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < min_numel:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} with at least {min_numel} elements")
 
 
@@ -479,13 +479,20 @@ class KvBatch:
         self.ref = ctypes.addressof(self.c)
 
 
-def _rows(t, name, batch, heads, dim):
+def _rows(t, name, n_rows, heads, dim):
     """Row stride of an fp16 [n_rows][heads][dim] tensor whose heads are contiguous."""
-    if t.dtype != torch.float16 or t.dim() != 3 or t.shape[0] < batch.n_rows or t.shape[1] != heads or \
-            t.shape[2] != dim or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"{name} must be fp16 [n_rows >= {batch.n_rows}][{heads}][{dim}] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    if t.dtype is torch.float16 and t.dim() == 3:
+        n, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if n >= n_rows and h == heads and d == dim and s2 == 1 and (s1 == dim or heads == 1):
+            return s0 if n > 1 else heads * dim
+    raise MoeError(MOE_ERR_INVALID_ARG,
+                   f"{name} must be fp16 [n_rows >= {n_rows}][{heads}][{dim}] with contiguous heads")
+
+
+def _kv_stream(s):
+    """As _stream, without building a Stream object for the current one."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if s is None else _stream(s)
 
 
 def _seqs(cache, n_seqs):
@@ -499,22 +506,24 @@ def moe_kv_check(kv, stream=None):
     _check(load().moe_kv_check(kv.handle, _stream(stream)))
 
 
-def moe_kv_append_q4(kv, cache: KvCache, batch: KvBatch, k, v, stream=None):
+def _kv_rows_call(fn, kv, cache, batch, k, v, stream):
     c = kv.cfg
-    _seqs(cache, batch.n_seqs)
-    _check(load().moe_kv_append_q4(kv.handle, cache.ref, batch.ref,
-                                   k.data_ptr(), _rows(k, "k", batch, c.n_kv_heads, c.head_dim),
-                                   v.data_ptr(), _rows(v, "v", batch, c.n_kv_heads, c.head_dim),
-                                   _stream(stream)))
+    n = batch.n_rows
+    if batch.n_seqs > cache.n_seqs:
+        _seqs(cache, batch.n_seqs)
+    rc = fn(kv.handle, cache.ref, batch.ref,
+            k.data_ptr(), _rows(k, "k", n, c.n_kv_heads, c.head_dim),
+            v.data_ptr(), _rows(v, "v", n, c.n_kv_heads, c.head_dim), _kv_stream(stream))
+    if rc:
+        _check(rc)
+
+
+def moe_kv_append_q4(kv, cache: KvCache, batch: KvBatch, k, v, stream=None):
+    _kv_rows_call(load().moe_kv_append_q4, kv, cache, batch, k, v, stream)
 
 
 def moe_kv_read_q4(kv, cache: KvCache, batch: KvBatch, k, v, stream=None):
-    c = kv.cfg
-    _seqs(cache, batch.n_seqs)
-    _check(load().moe_kv_read_q4(kv.handle, cache.ref, batch.ref,
-                                 k.data_ptr(), _rows(k, "k", batch, c.n_kv_heads, c.head_dim),
-                                 v.data_ptr(), _rows(v, "v", batch, c.n_kv_heads, c.head_dim),
-                                 _stream(stream)))
+    _kv_rows_call(load().moe_kv_read_q4, kv, cache, batch, k, v, stream)
 
 
 def moe_attn_q4(kv, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=1.0, window=0,
@@ -522,18 +531,24 @@ def moe_attn_q4(kv, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=1.0,
     """Attention of the batch's rows; weights=True also adds the weight that each
     entry received to the cache's scores (MOE_ATTN_WEIGHTS)."""
     c = kv.cfg
-    _seqs(cache, batch.n_seqs)
+    n, heads, dim = batch.n_rows, c.n_q_heads, c.head_dim
+    if batch.n_seqs > cache.n_seqs:
+        _seqs(cache, batch.n_seqs)
     if lse is not None:
-        _need(lse, "lse", torch.float32, batch.n_rows * c.n_q_heads)
-    _check(load().moe_attn_q4(kv.handle, cache.ref, batch.ref,
-                              q.data_ptr(), _rows(q, "q", batch, c.n_q_heads, c.head_dim), scale, window,
-                              MOE_ATTN_WEIGHTS if weights else 0,
-                              out.data_ptr(), _rows(out, "out", batch, c.n_q_heads, c.head_dim),
-                              _ptr(lse), _stream(stream)))
+        _need(lse, "lse", torch.float32, n * heads)
+    rc = load().moe_attn_q4(kv.handle, cache.ref, batch.ref,
+                            q.data_ptr(), _rows(q, "q", n, heads, dim), scale, window,
+                            MOE_ATTN_WEIGHTS if weights else 0,
+                            out.data_ptr(), _rows(out, "out", n, heads, dim),
+                            None if lse is None else lse.data_ptr(), _kv_stream(stream))
+    if rc:
+        _check(rc)
 
 
 def moe_kv_evict(kv, cache: KvCache, n_seqs, budget, n_recent, new_lens, stream=None):
     _seqs(cache, n_seqs)
     _need(new_lens, "new_lens", torch.int32, n_seqs)
-    _check(load().moe_kv_evict(kv.handle, cache.ref, n_seqs, budget, n_recent, new_lens.data_ptr(),
-                               _stream(stream)))
+    rc = load().moe_kv_evict(kv.handle, cache.ref, n_seqs, budget, n_recent, new_lens.data_ptr(),
+                             _kv_stream(stream))
+    if rc:
+        _check(rc)
