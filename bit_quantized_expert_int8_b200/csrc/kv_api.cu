@@ -1,6 +1,7 @@
 // kv_api.cu -- the C ABI of the 4-bit KV cache (declared in moeq4.h): argument
 // checks, workspace and launches.  The arithmetic runs in kv_cache.cuh and
 // kv_attn.cuh.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -70,18 +71,19 @@ struct moe_kv {
     float* part = nullptr;     // partial sums of the split attention
     int* count = nullptr;      // arrivals per cut item, zero between calls
     int split_ctas[2] = {0, 0};  // CTAs of the split kernel: 8-row and 16-row tiles
+    int split_smem[2] = {0, 0};
 };
 
 // The split kernel of one head size and row-tile count.
 typedef void (*SplitFn)(const SplitArgs);
 struct SplitKernel {
     SplitFn fn;
-    int smem, part_floats;
+    int smem, rows, part_floats;
 };
 template <int NG, int RT>
 static SplitKernel split_of() {
     using Sh = SplitShape<NG, RT>;
-    return {k_attn_split<NG, RT>, Sh::kSmem, Sh::kRows * (Sh::kD + 2)};
+    return {k_attn_split<NG, RT>, Sh::kSmem, Sh::kRows, Sh::kRows * (Sh::kD + 2)};
 }
 static SplitKernel split_kernel(int ng, int rt) {
     static const SplitKernel table[4][2] = {{split_of<1, 1>(), split_of<1, 2>()},
@@ -147,11 +149,18 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     for (int rt = 1; rt <= 2 && e == cudaSuccess; rt++) {
         const SplitKernel k = split_kernel(cfg->head_dim / 64, rt);
         int occ = 0;
-        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, k.fn);
+        const int most = optin - (int)fa.sharedSizeBytes;
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, kSplitThreads, k.smem);
         if (e == cudaSuccess && occ < 1) e = cudaErrorInvalidConfiguration;
         const size_t n = (size_t)kv->n_sms * (occ > 0 ? occ : 1);
         kv->split_ctas[rt - 1] = (int)n;
+        // an item may be cut into as many parts as there are CTAs: their weights and totals
+        // (two floats a row) have to fit as well
+        kv->split_smem[rt - 1] = std::max(k.smem, (int)n * k.rows * 8);
+        if (e == cudaSuccess && kv->split_smem[rt - 1] > most) e = cudaErrorInvalidConfiguration;
         if (2 * n * k.part_floats > part) part = 2 * n * k.part_floats;
         if (n > ctas) ctas = n;
     }
@@ -306,7 +315,8 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     x.max_rows_seq = 1 << 30;
     const int rt = a.c.max_q * (a.c.hq / a.c.hkv) <= 8 ? 1 : 2;
     const SplitKernel k = split_kernel(a.c.ng, rt);
-    KV_CK(kv_launch(k.fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads, k.smem, stream, x));
+    KV_CK(kv_launch(k.fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads, kv->split_smem[rt - 1],
+                    stream, x));
     if (flags & MOE_ATTN_WEIGHTS)
         KV_CK(kv_launch(k_attn_weights_simple, dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream, a));
     return MOE_OK;

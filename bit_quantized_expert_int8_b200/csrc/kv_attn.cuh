@@ -655,25 +655,62 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
             if (tid == 0) s_last = atomicAdd(x.count + c0, 1) == c1 - c0;
             __syncthreads();
             if (s_last) {
+                // every part's maximum and total at once, then its weight, then the sums of up to
+                // eight parts in flight per thread
                 __threadfence();
-                for (int k = tid; k < R * (D / 8); k += kSplitThreads) {
-                    const int r = k / (D / 8), d = (k % (D / 8)) * 8;
-                    if (rt * R + r >= rows) continue;
-                    float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    const auto at = [&](int b) { return x.part + (size_t)(2 * b + (b == c0 ? 1 : 0)) * (R * (D + 2)); };
-                    for (int b = c0; b <= c1; b++) M = fmaxf(M, __ldcg(at(b) + R * D + r));
+                const int parts = c1 - c0 + 1;
+                float* pf = reinterpret_cast<float*>(sp_smem);           // [parts][R] weight (first the maximum)
+                float* pl = pf + parts * R;                              // [parts][R] total
+                const auto at = [&](int b) { return x.part + (size_t)(2 * (c0 + b) + (b == 0 ? 1 : 0)) * (R * (D + 2)); };
+                for (int k = tid; k < parts * R; k += kSplitThreads) {
+                    const float* src = at(k / R) + R * D + k % R;
+                    pf[k] = __ldcg(src);
+                    pl[k] = __ldcg(src + R);
+                }
+                __syncthreads();
+                for (int r = warp; r < R; r += kSplitWarps) {
+                    float M = -INFINITY, L = 0.f;
+                    for (int b = lane; b < parts; b += 32) M = fmaxf(M, pf[b * R + r]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
                     const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-                    for (int b = c0; b <= c1; b++) {
-                        const float* src = at(b);
-                        const float mb = __ldcg(src + R * D + r), lb = __ldcg(src + R * D + R + r);
-                        const float4 v0 = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + d));
-                        const float4 v1 = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + d) + 1);
+                    for (int b = lane; b < parts; b += 32) {
+                        const float mb = pf[b * R + r], lb = pl[b * R + r];
                         const float f = mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref);
+                        pf[b * R + r] = f;
                         L = fmaf(f, lb, L);
-                        add(o, f, v0, v1);
                     }
-                    store_row(rt * R + r, d, o, M, L);
+                    L = warp_sum(L);
+                    if (lane == 0) {
+                        s_m[0][r] = M;
+                        s_l[0][r] = L;
+                    }
+                }
+                __syncthreads();
+                for (int k = tid; k < R * (D / 4); k += kSplitThreads) {
+                    const int r = k / (D / 4), d = (k % (D / 4)) * 4;
+                    if (rt * R + r >= rows) continue;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int b0 = 0; b0 < parts; b0 += 8) {
+                        float4 v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[e] = b0 + e < parts ? __ldcg(reinterpret_cast<const float4*>(at(b0 + e) + (size_t)r * D + d))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float f = b0 + e < parts ? pf[(b0 + e) * R + r] : 0.f;
+                            o.x = fmaf(f, v[e].x, o.x);
+                            o.y = fmaf(f, v[e].y, o.y);
+                            o.z = fmaf(f, v[e].z, o.z);
+                            o.w = fmaf(f, v[e].w, o.w);
+                        }
+                    }
+                    const int i = (rt * R + r) / G, head = h * G + (rt * R + r) % G;
+                    const float M = s_m[0][r], L = s_l[0][r], f = L == 0.f ? 0.f : 1.f / L;
+                    *reinterpret_cast<uint2*>(a.out + (size_t)(q.first + i) * a.out_stride + (size_t)head * D + d) =
+                        make_uint2(f2h(o.x * f, o.y * f), f2h(o.z * f, o.w * f));
+                    if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                 }
                 if (tid == 0) x.count[c0] = 0;
             }
