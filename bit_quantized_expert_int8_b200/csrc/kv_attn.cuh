@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     constexpr int R = Sh::kRows, D = Sh::kD, JR = Sh::kJoinRow;
     extern __shared__ __align__(128) uint8_t sp_smem[];
     __shared__ float s_m[kSplitWarps][R], s_l[kSplitWarps][R], s_qs[NG][R], s_sl2[R];
-    __shared__ long long s_plan[2];
+    __shared__ long long s_base0, s_total, s_per;
+    __shared__ SplitSeq s_q;
     __shared__ int s_seq, s_last;
     const AttnArgs& a = x.a;
     const KvArgs& c = a.c;
@@ -361,20 +362,24 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
     // units of all sequences, this CTA's range and the sequence it begins in
     if (warp == 0) {
         long long total = 0;
+        SplitSeq q{};
         for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-            const int s = s0 + lane;
-            total += s < c.n_seqs ? split_seq<R>(x, s, blockIdx.x == 0).units : 0;
+            q.units = 0;
+            if (s0 + lane < c.n_seqs) q = split_seq<R>(x, s0 + lane, blockIdx.x == 0);
+            total += q.units;
         }
         total = warp_sum(total);
-        const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kSplitMinUnits);
+        const long long n = total + gridDim.x - 1;
+        const long long per = max(n >> 32 ? n / gridDim.x : (long long)((unsigned)n / gridDim.x), (long long)kSplitMinUnits);
         const long long u = blockIdx.x * per;
-        int s = 0;
         long long base = 0;
         if (u < total)
             for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-                const int sl = s0 + lane;
-                const int w = sl < c.n_seqs ? split_seq<R>(x, sl, false).units : 0;
-                long long inc = w;
+                if (c.n_seqs > 32) {                         // else q holds it already
+                    q.units = 0;
+                    if (s0 + lane < c.n_seqs) q = split_seq<R>(x, s0 + lane, false);
+                }
+                long long inc = q.units;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -382,27 +387,27 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                 }
                 const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
                 if (hit) {
-                    const int at = __ffs(hit) - 1;
-                    s = s0 + at;
-                    base += __shfl_sync(0xffffffffu, inc - w, at);
+                    if (lane == __ffs(hit) - 1) {
+                        s_q = q;
+                        s_seq = s0 + lane;
+                        s_base0 = base + inc - q.units;
+                    }
                     break;
                 }
                 base += __shfl_sync(0xffffffffu, inc, 31);
             }
         if (lane == 0) {
-            s_plan[0] = total;
-            s_plan[1] = base;
-            s_seq = s;
+            s_total = total;
+            s_per = per;
         }
     }
     __syncthreads();
-    const long long total = s_plan[0];
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kSplitMinUnits);
-    long long u = blockIdx.x * per, s_base = s_plan[1];
+    const long long total = s_total, per = s_per;
+    long long u = blockIdx.x * per, s_base = s_base0;
     const long long u_end = min(total, u + per);
     if (u >= u_end) return;
     int s = s_seq;
-    SplitSeq q = split_seq<R>(x, s, false);
+    SplitSeq q = s_q;
 
     const uint32_t ring = smem_u32(sp_smem) + warp * (kSplitStages * Sh::kHalf);
     const int half = warp & 1, par = warp >> 1;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
             s++;
             q = split_seq<R>(x, s, false);
         }
-        const int item = (int)(u - s_base) / (q.np + kSplitItemCost);
+        const int item = (int)(u - s_base) / (q.np + kSplitItemCost);        // within one sequence: 32 bits
         // the item's pages stand at units ib .. ie - 1, behind its fixed cost
         const long long ib = s_base + (long long)item * (q.np + kSplitItemCost) + kSplitItemCost, ie = ib + q.np;
         u = max(u, ib);
@@ -441,6 +446,19 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         const int rows = q.n * G;
         u = min(u_end, ie);
 
+        // queries of the tile: threads 4 r + t take 16 columns of each group of row r
+        const int qt = tid & 3, qr = tid >> 2;
+        uint4 qv[NG][2];
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+            qv[g][0] = qv[g][1] = make_uint4(0, 0, 0, 0);
+            if (qr < R && rt * R + qr < rows) {
+                const int rr = rt * R + qr;
+                const __half* qp = a.q + (size_t)(q.first + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + g * 64 + qt * 16;
+                qv[g][0] = *reinterpret_cast<const uint4*>(qp);
+                qv[g][1] = *reinterpret_cast<const uint4*>(qp + 8);
+            }
+        }
         // the stage holds this warp's half of page pg0 + par + kStep k
         unsigned ok = 0;                                     // bit: the stage's page is usable
         const int32_t* trow = c.table + (size_t)s * c.max_pages;
@@ -473,22 +491,14 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
 #pragma unroll
         for (int st = 0; st < kSplitStages - 1; st++) fetch(pg0 + par + kStep * st, st);
 
-        // queries of the tile into the operand order of code_pairs: per group, 4 steps of
-        // 16 columns; lane (g8, t4) holds columns 16 t4 + m (+ 4, + 8, + 12) of rows g8, g8 + 8
+        // into the operand order of code_pairs: per group, 4 steps of 16 columns; lane
+        // (g8, t4) holds columns 16 t4 + m (+ 4, + 8, + 12) of rows g8, g8 + 8
         if (tid < R * 4) {
-            const int t = tid & 3, r = tid >> 2;
-            uint4 v[NG][2];
+            const int t = qt, r = qr;
             float mx = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; g++) {
-                v[g][0] = v[g][1] = make_uint4(0, 0, 0, 0);
-                if (rt * R + r < rows) {
-                    const int rr = rt * R + r;
-                    const __half* qp = a.q + (size_t)(q.first + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + g * 64 + t * 16;
-                    v[g][0] = *reinterpret_cast<const uint4*>(qp);
-                    v[g][1] = *reinterpret_cast<const uint4*>(qp + 8);
-                }
-                const uint32_t w[8] = {v[g][0].x, v[g][0].y, v[g][0].z, v[g][0].w, v[g][1].x, v[g][1].y, v[g][1].z, v[g][1].w};
+                const uint32_t w[8] = {qv[g][0].x, qv[g][0].y, qv[g][0].z, qv[g][0].w, qv[g][1].x, qv[g][1].y, qv[g][1].z, qv[g][1].w};
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const float2 f = h2f(w[k]);
@@ -507,7 +517,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const uint4 x4 = v[g][e];
+                    const uint4 x4 = qv[g][e];
                     const uint32_t w[4] = {__byte_perm(x4.x, x4.z, 0x5410), __byte_perm(x4.x, x4.z, 0x7632),
                                            __byte_perm(x4.y, x4.w, 0x5410), __byte_perm(x4.y, x4.w, 0x7632)};
 #pragma unroll
@@ -656,7 +666,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
             __syncthreads();
             if (s_last) {
                 // every part's maximum and total at once, then its weight, then the sums of up to
-                // eight parts in flight per thread
+                // sixteen parts in flight per thread
                 __threadfence();
                 const int parts = c1 - c0 + 1;
                 float* pf = reinterpret_cast<float*>(sp_smem);           // [parts][R] weight (first the maximum)
@@ -691,14 +701,14 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                     const int r = k / (D / 4), d = (k % (D / 4)) * 4;
                     if (rt * R + r >= rows) continue;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int b0 = 0; b0 < parts; b0 += 8) {
-                        float4 v[8];
+                    for (int b0 = 0; b0 < parts; b0 += 16) {
+                        float4 v[16];
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
+                        for (int e = 0; e < 16; e++)
                             v[e] = b0 + e < parts ? __ldcg(reinterpret_cast<const float4*>(at(b0 + e) + (size_t)r * D + d))
                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int e = 0; e < 8; e++) {
+                        for (int e = 0; e < 16; e++) {
                             const float f = b0 + e < parts ? pf[(b0 + e) * R + r] : 0.f;
                             o.x = fmaf(f, v[e].x, o.x);
                             o.y = fmaf(f, v[e].y, o.y);
