@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "kv_attn.cuh"
+#include "kv_attn_tc.cuh"
 #include "kv_cache.cuh"
 
 using namespace moeq4;
@@ -66,12 +67,14 @@ struct moe_kv {
     int n_sms = 0;
     size_t smem_optin = 0;
     uint8_t* ws = nullptr;
-    int* status = nullptr;
+    int* status = nullptr;     // [2]: what kernels report, a bounded wait that gave up
     float* lse = nullptr;      // [max_rows][n_q_heads], where the caller wants none
     float* part = nullptr;     // partial sums of the split attention
     int* count = nullptr;      // arrivals per cut item, zero between calls
     int split_ctas[2] = {0, 0};  // CTAs of the split kernel: 8-row and 16-row tiles
     int split_smem[2] = {0, 0};
+    int tile_smem = 0;         // of the tile kernel; 0 where no call can have enough rows for it
+    size_t counts = 0;         // length of count
 };
 
 // The split kernel of one head size and row-tile count.
@@ -84,6 +87,19 @@ template <int NG, int RT>
 static SplitKernel split_of() {
     using Sh = SplitShape<NG, RT>;
     return {k_attn_split<NG, RT>, Sh::kSmem, Sh::kRows, Sh::kRows * (Sh::kD + 2)};
+}
+typedef void (*TileFn)(const TileArgs);
+struct TileKernel {
+    TileFn fn;
+    int smem, part_floats;
+};
+template <int NG>
+static TileKernel tile_of() {
+    return {k_attn_tile<NG>, TileShape<NG>::kSmem, kTileRows * (TileShape<NG>::kD + 2)};
+}
+static TileKernel tile_kernel(int ng) {
+    static const TileKernel table[4] = {tile_of<1>(), tile_of<2>(), tile_of<3>(), tile_of<4>()};
+    return table[ng - 1];
 }
 static SplitKernel split_kernel(int ng, int rt) {
     static const SplitKernel table[4][2] = {{split_of<1, 1>(), split_of<1, 2>()},
@@ -142,7 +158,7 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     kv->smem_optin = (size_t)optin;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off = (off + bytes + 255) / 256 * 256; return o; };
-    const size_t o_status = take(sizeof(int));
+    const size_t o_status = take(2 * sizeof(int));
     const size_t o_lse = take((size_t)cfg->max_rows * cfg->n_q_heads * sizeof(float));
     // every kernel's shared memory limit is raised here: no later call changes it
     size_t part = 0, ctas = 0;
@@ -164,8 +180,15 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
         if (2 * n * k.part_floats > part) part = 2 * n * k.part_floats;
         if (n > ctas) ctas = n;
     }
+    if (e == cudaSuccess && (int64_t)cfg->max_rows * (cfg->n_q_heads / cfg->n_kv_heads) > kSplitMaxRows) {
+        const TileKernel k = tile_kernel(cfg->head_dim / 64);
+        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        part = std::max(part, (size_t)2 * kv->n_sms * k.part_floats);
+        kv->tile_smem = k.smem;
+    }
     const size_t o_part = take(part * sizeof(float));
     const size_t o_count = take(ctas * sizeof(int));
+    kv->counts = ctas;
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
     if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
@@ -185,11 +208,15 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
 extern "C" int moe_kv_check(moe_kv* kv, moe_stream_t stream) {
     if (!kv) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_check: NULL context");
     KV_CK(cudaStreamSynchronize(stream));
-    int st = 0;
-    KV_CK(cudaMemcpy(&st, kv->status, sizeof(int), cudaMemcpyDeviceToHost));
-    if (st == 0) return MOE_OK;
-    KV_CK(cudaMemset(kv->status, 0, sizeof(int)));
-    return kv_fail(st, "a KV cache kernel met a length, row start or page index outside its limits");
+    int st[2] = {0, 0};
+    KV_CK(cudaMemcpy(st, kv->status, sizeof(st), cudaMemcpyDeviceToHost));
+    if (st[0] == 0 && st[1] == 0) return MOE_OK;
+    KV_CK(cudaMemset(kv->status, 0, sizeof(st)));
+    if (st[1] != 0) {                  // some CTAs left early: the arrival counts begin anew
+        KV_CK(cudaMemset(kv->count, 0, kv->counts * sizeof(int)));
+        return kv_fail(st[1], "a bounded device wait of an attention call gave up; its outputs are not valid");
+    }
+    return kv_fail(st[0], "a KV cache kernel met a length, row start or page index outside its limits");
 }
 
 static int kv_check_device(const moe_kv* kv, const char* who) {
@@ -241,6 +268,7 @@ static KvArgs kv_args(const moe_kv* kv, const MoeKvCache* c, const MoeKvBatch* b
     a.pos = c->pos;
     a.seen = c->seen;
     a.status = kv->status;
+    a.stop = kv->status + 1;
     a.n_seqs = n_seqs;
     a.n_rows = b ? b->n_rows : 0;
     a.max_q = b ? (b->max_q < b->n_rows ? b->max_q : b->n_rows) : 0;
@@ -308,15 +336,21 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     a.out_stride = out_stride;
     a.scale = scale;
     a.window = window;
-    SplitArgs x{};
-    x.a = a;
-    x.part = kv->part;
-    x.count = kv->count;
-    x.max_rows_seq = 1 << 30;
-    const int rt = a.c.max_q * (a.c.hq / a.c.hkv) <= 8 ? 1 : 2;
-    const SplitKernel k = split_kernel(a.c.ng, rt);
-    KV_CK(kv_launch(k.fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads, kv->split_smem[rt - 1],
-                    stream, x));
+    // sequences of many rows on the tile kernel, of few on the split kernel (each passes over
+    // the other's); one sequence needs one of them
+    const int64_t most = (int64_t)a.c.max_q * (a.c.hq / a.c.hkv);
+    const bool tile = most > kSplitMaxRows;
+    if (tile) {
+        TileArgs y{a, kv->part, kv->count, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
+        const TileKernel k = tile_kernel(a.c.ng);
+        KV_CK(kv_launch(k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
+    }
+    if (!tile || a.c.n_seqs > 1) {
+        const int rt = most <= 8 ? 1 : 2;
+        SplitArgs x{a, kv->part, kv->count, kSplitMaxRows};
+        KV_CK(kv_launch(split_kernel(a.c.ng, rt).fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads,
+                        kv->split_smem[rt - 1], stream, x));
+    }
     if (flags & MOE_ATTN_WEIGHTS)
         KV_CK(kv_launch(k_attn_weights_simple, dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream, a));
     return MOE_OK;

@@ -106,6 +106,7 @@ constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitStages = 3;
 constexpr int kSplitMinUnits = 4;      // pages per CTA at least: fewer partial sums in small calls
 constexpr int kSplitItemCost = 4;
+constexpr int kSplitMaxRows = 16;      // (row, head) pairs per kv head: more go to the tile kernel
 
 template <int NG, int RT>
 struct SplitShape {

@@ -27,7 +27,8 @@ struct KvArgs {
     float* score;
     int32_t* pos;
     const int32_t* seen;
-    int* status;
+    int* status;               // what kv_flag reports
+    int* stop;                 // a bounded wait gave up
     int n_seqs, n_rows, max_q, hq, hkv, ng, n_pages, max_pages;
 };
 

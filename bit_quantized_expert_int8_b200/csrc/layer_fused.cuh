@@ -47,6 +47,7 @@
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
+#include "wait.cuh"
 
 namespace moeq4 {
 
@@ -62,7 +63,6 @@ constexpr int kMaxDownItems = 4;            // routed down items one CTA keeps r
 constexpr int kRdRows = 16;                 // output rows per routed down item (one down tile)
 constexpr int kSdRows = 32;                 // output rows per shared down item (two down tiles)
 constexpr int kRedFloats = kFusedConsumerWarps * kRdRows;   // per-stage cross-warp sums
-constexpr unsigned long long kWaitNs = 2000000000ull;   // bound of every device wait (2 s)
 
 // Work classes a launch may include (bit mask).
 enum : int { kModeRouter = 1, kModeShared = 2, kModeRouted = 4, kModeDown = 8,
@@ -142,12 +142,6 @@ constexpr int kTracePhase = 32;
 constexpr int kTraceItems = (kTraceWords - kTracePhase) / 3;
 constexpr unsigned long long kTraceTimeMask = (1ull << 56) - 1;
 
-__device__ __forceinline__ unsigned long long gtimer_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
 __device__ __forceinline__ void fused_trace(const FusedArgs& a, int slot) {
     if (a.trace) a.trace[(size_t)blockIdx.x * kTraceWords + slot] = gtimer_ns();
 }
@@ -161,32 +155,6 @@ __device__ __forceinline__ void fused_trace_item(const FusedArgs& a, int item, i
 }
 
 // ------------------------------------------------------------- waiting --
-__device__ __forceinline__ void fused_fail(int* status) { atomicCAS(status, 0, MOE_ERR_TIMEOUT); }
-
-__device__ __forceinline__ bool fused_aborted(const int* status) {
-    return ld_relaxed_s32(status) != 0;
-}
-
-// Waits longer than this look at the status word in global memory (a load
-// that can take microseconds under load, so ordinary waits never issue it).
-constexpr unsigned long long kAbortCheckNs = 20000;
-
-// Wait on an mbarrier phase, bounded in time; once the wait is long, gives up
-// early when another thread has already recorded a failure.
-__device__ __forceinline__ bool fused_wait_bar(uint64_t* bar, uint32_t parity, int* status,
-                                               unsigned long long bound = kWaitNs) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = gtimer_ns();
-    for (unsigned it = 1;; it++) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31) == 0) {
-            const unsigned long long el = gtimer_ns() - t0;
-            if (el > bound) { fused_fail(status); return false; }
-            if (el > kAbortCheckNs && fused_aborted(status)) return false;
-        }
-    }
-}
-
 // Wait until *p >= target, bounded in time.
 __device__ __forceinline__ bool fused_wait_ge(const unsigned long long* p,
                                               unsigned long long target, int* status,

@@ -10,6 +10,13 @@ far end of its distribution.  The weighted sum adds 16-entry steps of at most
 1e-4 relative (1e-6 absolute) on accumulated weights, and on the output 1e-4
 beside the half step 2^-11 of its rounding to fp16 (2^-25 below the normal
 range).
+
+Sequences with more than 16 (row, head) pairs per kv head take p s, the weight
+times the scale of a group, as one fp16 operand: it is off by at most half a
+step, 2^-11 of its size, and multiplies code - 8.  An output is sum_j p_j s_j
+(code_j - 8) + p_j (bias_j + 8 s_j) over sum p, so this adds at most 2^-11 sum_j
+w_j |s_j (code_j - 8)| with the weights w = p / sum p: the attention of
+|V - (bias + 8 scale)|, which the reference forms.
 """
 import math
 
@@ -81,7 +88,7 @@ class Case:
         return (self.rng.standard_normal((self.n_rows, self.Hq, self.D)) * 1.5).astype(np.float16)
 
     def reference(self, q, scale, window=0):
-        out = np.zeros((self.n_rows, self.Hq, self.D))
+        out, spread = np.zeros((2, self.n_rows, self.Hq, self.D))
         lse = np.full((self.n_rows, self.Hq), -np.inf)
         got = np.zeros((self.n, self.Hkv, self.cap))
         for s in range(self.n):
@@ -90,7 +97,10 @@ class Case:
                 continue
             K, V = kv_ref.sequence(self.pages, self.table[s], n, self.Hkv, self.D)
             out[a:b], lse[a:b], got[s, :, :n] = kv_ref.attention(q[a:b].astype(np.float64), K, V, scale, window, n)
-        return out, lse, got
+            if (b - a) * self.Hq // self.Hkv > 16:
+                U = kv_ref.value_spread(self.pages, self.table[s], V, self.D)
+                spread[a:b] = kv_ref.attention(q[a:b].astype(np.float64), K, U, scale, window, n)[0]
+        return out, lse, got, spread
 
     def attend(self, q, scale, window=0, weights=False, **kw):
         out = torch.full((self.n_rows, self.Hq, self.D), 7.0, dtype=torch.float16, device=DEV)
@@ -102,10 +112,11 @@ class Case:
 
 
 def close(out, lse, ref, rows=None):
-    ro, rl = ref[0][:rows], ref[1][:rows]
+    ro, rl, rs = ref[0][:rows], ref[1][:rows], ref[3][:rows]
     out, lse = out[:rows], lse[:rows]
     assert np.isfinite(out).all()
-    assert (np.abs(out - ro) <= 2.0 ** -11 * np.abs(ro) + 2.0 ** -25 + 1e-4).all(), np.abs(out - ro).max()
+    off = np.abs(out - ro) - (2.0 ** -11 * (np.abs(ro) + rs) + 2.0 ** -25 + 1e-4)
+    assert (off <= 0).all(), off.max()
     dead = np.isneginf(rl)
     assert (np.isneginf(lse) == dead).all()
     assert (np.abs(lse[~dead] - rl[~dead]) <= 1e-4).all(), np.abs(lse[~dead] - rl[~dead]).max()
@@ -199,7 +210,7 @@ def test_small_and_large_values(sigma):
     # q / sigma is rounded to fp16 (subnormal for 300) on both sides alike; the
     # code offset makes partial sums of the bias part about as large as above.
     # At 1e-4 the output itself is in fp16's subnormal range, where a half step is 2^-25
-    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * np.abs(ref[0]) + 2.0 ** -25 + 1e-4 * sigma).all()
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 2.0 ** -25 + 1e-4 * sigma).all()
     assert (np.abs(lse - ref[1]) <= 1e-4).all()
 
 
@@ -327,7 +338,7 @@ def test_pool_offsets_beyond_32_bits():
     moeq4.moe_attn_q4(kv, cache, batch, cu(q), out, lse=lse, scale=0.06)
     moeq4.moe_kv_check(kv)
     K, V = kv_ref.sequence(small, [0, 1, 2, 3], 250, Hkv, D)
-    ref = kv_ref.attention(q.astype(np.float64), K, V, 0.06, 0, 250)
+    ref = (*kv_ref.attention(q.astype(np.float64), K, V, 0.06, 0, 250), np.zeros((1, 8, D)))
     close(out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), ref)
     assert np.array_equal(pool[at[3] * per:(at[3] + 1) * per].cpu().numpy(), small[3].reshape(-1))
 
@@ -472,7 +483,9 @@ def test_bounded_decode_steps():
                 pos[s, :, at] = seen[s] - rows[s] + i
             K, V = kv_ref.sequence(pages, table[s], int(lens[s]), Hkv, D)
             ro, rl, w = kv_ref.attention(qkv[a:b, :Hq].astype(np.float64), K, V, 0.09, 0, int(lens[s]))
-            close(out[a:b].cpu().numpy().astype(np.float64), lse[a:b].cpu().numpy().astype(np.float64), (ro, rl))
+            U = kv_ref.value_spread(pages, table[s], V, D) if rows[s] * Hq // Hkv > 16 else 0 * V
+            rs = kv_ref.attention(qkv[a:b, :Hq].astype(np.float64), K, U, 0.09, 0, int(lens[s]))[0]
+            close(out[a:b].cpu().numpy().astype(np.float64), lse[a:b].cpu().numpy().astype(np.float64), (ro, rl, w, rs))
             score64[s, :, :lens[s]] += w
             lens[s] = kv_ref.evict(pages, table[s], int(lens[s]), int(seen[s]), score64[s], pos[s], budget, recent)
         assert glens[nxt].cpu().tolist() == lens.tolist()
