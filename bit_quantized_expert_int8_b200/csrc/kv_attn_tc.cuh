@@ -17,14 +17,14 @@
 // by more than 2^8, and only then is O rescaled.
 //
 // Roles, meeting at mbarriers (every wait bounded):
-//   warps 0..7    scores and softmax: warp w holds rows 32 (w % 4) .. of the tile
-//                 (TMEM lanes) and half w / 4 of its entries; the two halves of a
-//                 row exchange their maximum through shared memory;
-//   warps 8..11   converters: codes from global memory (the next tile's loads in
+//   warps 0..15   scores and softmax: warp w holds rows 32 (w % 4) .. of the tile
+//                 (TMEM lanes) and quarter w / 4 of its entries; the four quarters
+//                 of a row exchange their maximum through shared memory;
+//   warps 16..19  converters: codes from global memory (the next tile's loads in
 //                 flight while one is converted) to fp16 operands in shared memory,
 //                 128-byte swizzle: K entry-major, V transposed (8 x 8 blocks of
 //                 codes turned in registers); scales and biases to fp32;
-//   warp 12       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
+//   warp 20       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
 //                 tile t, so it runs under the softmax of tile t.
 // Work is cut and joined as in the split kernel: equal runs of pages per CTA,
 // partial sums in the workspace, the last CTA to arrive joins an item.
@@ -36,18 +36,24 @@
 namespace moeq4 {
 
 constexpr int kTileRows = 128;
-constexpr int kTileWarps = 13;
+constexpr int kTileSoft = 16;          // softmax warps: 4 per 32 rows
+constexpr int kTileWarps = kTileSoft + 5;
 constexpr int kTileThreads = kTileWarps * 32;
 constexpr int kTileSlots = 3;
 constexpr int kTileItemCost = 4;       // pages an item costs beside its own
 constexpr int kTileMinUnits = 6;       // pages per CTA at least
+
+template <bool B>
+struct BoolC {
+    static constexpr bool value = B;
+};
 
 template <int NG>
 struct TileShape {
     static constexpr int kD = 64 * NG;
     static constexpr int KT = NG <= 2 ? 64 : 32;                // entries per tile
     static constexpr int kSub = kKvPage / KT;                   // tiles per page
-    static constexpr int kHK = KT / 2;                          // entries per softmax thread
+    static constexpr int kHK = KT / 4;                          // entries per softmax thread
     static constexpr int kQ = NG * kTileRows * 128;             // bytes
     static constexpr int kK = NG * KT * 128;
     static constexpr int kV = NG * 64 * 128;                    // 64 columns x KT entries, rows of 128 bytes
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     extern __shared__ uint8_t tl_raw[];
     __shared__ __align__(8) uint64_t b_full[kTileSlots], b_s[2], b_p[2], b_pv[2];
     __shared__ uint32_t s_tmem;
-    __shared__ float s_mx[2][2][kTileRows], s_qs[NG][kTileRows], s_sum[2][NG + 1][kTileRows];
+    __shared__ float s_mx[2][4][kTileRows], s_qs[NG][kTileRows];
     __shared__ float s_vmax[kTileSlots][4];
     __shared__ int s_ok[kTileSlots];
     __shared__ long long s_base0, s_total, s_per;
@@ -132,6 +138,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     uint8_t* gbase = tl_raw + (sbase - smem_u32(tl_raw));
     const uint32_t sQ = sbase, sSlots = sbase + Sh::kQ;
     uint8_t* gQ = gbase;
+    float(*s_sum)[NG + 1][kTileRows] = reinterpret_cast<float(*)[NG + 1][kTileRows]>(gQ);   // once Q has been used
     uint8_t* gSlots = gbase + Sh::kQ;
     float2* gScale = reinterpret_cast<float2*>(gSlots + kTileSlots * Sh::kSlot);   // [slot][K, V][g][entry]
 
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
         for (int i = 0; i < kTileSlots; i++) mbar_init(&b_full[i], 4);      // converter warps
         for (int i = 0; i < 2; i++) {
             mbar_init(&b_s[i], 1);                                          // commits
-            mbar_init(&b_p[i], 8);                                          // softmax warps
+            mbar_init(&b_p[i], kTileSoft);                                  // softmax warps
             mbar_init(&b_pv[i], 1);
         }
         fence_mbar_init();
@@ -263,9 +270,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
         fence_proxy_async_shared();
         __syncthreads();
 
-        if (warp < 8) {
+        if (warp < kTileSoft) {
             // ------------------------------------------------------ softmax --
-            const int q4 = warp & 3, half = warp >> 2, r = 32 * q4 + lane;
+            const int q4 = warp & 3, part = warp >> 2, r = 32 * q4 + lane;
             const uint32_t t_row = tmem + ((uint32_t)(32 * q4) << 16);
             const int rr = min(rt * kTileRows + r, q.rows - 1);
             const int pos = p0 + rr / G, low = a.window > 0 ? pos - a.window + 1 : 0;
@@ -284,32 +291,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 if (ok) ok = __all_sync(0xffffffffu, fused_wait_bar(&b_full[slot], (n / kTileSlots) & 1u, c.stop) &&
                                                          fused_wait_bar(&b_s[st], (n >> 1) & 1u, c.stop));
                 if (!ok) {                               // the others may still come to the barrier
-                    named_bar(1, 256);
+                    named_bar(1 + q4, 128);
                     continue;
                 }
                 tc_fence_after();
-                const float4* sk = reinterpret_cast<const float4*>(gScale + (size_t)slot * 2 * NG * KT) + half * (HK / 2);
+                const float4* sk = reinterpret_cast<const float4*>(gScale + (size_t)slot * 2 * NG * KT) + part * (HK / 2);
                 const float4* sv = sk + NG * KT / 2;
                 float S[HK];
-#pragma unroll
-                for (int b = 0; b < HK / 16; b++) {
-                    uint32_t acc[NG][16];
-#pragma unroll
-                    for (int g = 0; g < NG; g++) tmem_ld16_nw(t_s + g * KT + half * HK + b * 16, acc[g]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; j++) S[b * 16 + j] = 0.f;
+                {
+                    uint32_t acc[NG][HK];
 #pragma unroll
                     for (int g = 0; g < NG; g++)
 #pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const float4 f = sk[g * (KT / 2) + b * 8 + j];      // two entries
-                            float* o = S + b * 16 + 2 * j;
-                            o[0] = fmaf(f.x, __uint_as_float(acc[g][2 * j]), fmaf(f.y, qs[g], o[0]));
-                            o[1] = fmaf(f.z, __uint_as_float(acc[g][2 * j + 1]), fmaf(f.w, qs[g], o[1]));
+                        for (int b = 0; b < HK / 8; b++) tmem_ld8_nw(t_s + g * KT + part * HK + b * 8, acc[g] + b * 8);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < HK; j++) S[j] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < NG; g++)
+#pragma unroll
+                        for (int j = 0; j < HK / 2; j++) {
+                            const float4 f = sk[g * (KT / 2) + j];      // two entries
+                            S[2 * j] = fmaf(f.x, __uint_as_float(acc[g][2 * j]), fmaf(f.y, qs[g], S[2 * j]));
+                            S[2 * j + 1] = fmaf(f.z, __uint_as_float(acc[g][2 * j + 1]), fmaf(f.w, qs[g], S[2 * j + 1]));
                         }
                 }
-                const int j0 = (pg0 + t / Sh::kSub) * kKvPage + (t % Sh::kSub) * KT + half * HK;
+                const int j0 = (pg0 + t / Sh::kSub) * kKvPage + (t % Sh::kSub) * KT + part * HK;
                 const bool edge = j0 + HK - 1 > first_pos || j0 < last_low || !s_ok[slot];
                 uint32_t vis = 0xFFFFFFFFu;
                 if (edge) {
@@ -324,9 +331,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 float top = S[0];
 #pragma unroll
                 for (int j = 1; j < HK; j++) top = fmaxf(top, S[j]);
-                s_mx[st][half][r] = top;
-                named_bar(1, 256);
-                top = fmaxf(top, s_mx[st][half ^ 1][r]) * sl2;
+                s_mx[st][part][r] = top;
+                named_bar(1 + q4, 128);
+                top = fmaxf(fmaxf(s_mx[st][0][r], s_mx[st][1][r]), fmaxf(s_mx[st][2][r], s_mx[st][3][r])) * sl2;
                 // a scale of V beyond the present unit (alike in all threads)
                 const float* vm = s_vmax[slot];
                 const float vmax = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
@@ -344,14 +351,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     l *= f;
 #pragma unroll
                     for (int g = 0; g < NG; g++) B[g] *= f;
-                    if (t > 0) {                         // O so far: this half's columns of the row
+                    if (t > 0) {                         // O so far: this quarter's columns of the row
                         ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1u, c.stop));
                         if (!ok) continue;
                         tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < NG * 2; k++) {
+                        for (int k = 0; k < NG; k++) {
                             uint32_t o[16];
-                            const uint32_t at = t_row + Sh::kO + half * (NG * 32) + k * 16;
+                            const uint32_t at = t_row + Sh::kO + part * (NG * 16) + k * 16;
                             tmem_ld16_nw(at, o);
                             tmem_ld_wait();
 #pragma unroll
@@ -367,45 +374,43 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 #pragma unroll
                 for (int j = 4; j < HK; j++) ls[j & 3] += S[j];
                 l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                const auto store = [&](auto some) {
+                    constexpr bool EDGE = decltype(some)::value;
 #pragma unroll
-                for (int g = 0; g < NG; g++) {
-                    uint32_t P[HK / 2];
-                    float b2[2] = {0.f, 0.f};
+                    for (int g = 0; g < NG; g++) {
+                        uint32_t P[HK / 2];
+                        float b2[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < HK / 2; j++) {
-                        const float4 f = sv[g * (KT / 2) + j];
-                        float e0 = S[2 * j] * f.x, e1 = S[2 * j + 1] * f.z;
-                        if (edge) {                      // an entry out of sight may hold a NaN scale
-                            const bool v0 = (vis >> (2 * j)) & 1u, v1 = (vis >> (2 * j + 1)) & 1u;
-                            e0 = v0 ? e0 : 0.f;
-                            e1 = v1 ? e1 : 0.f;
+                        for (int j = 0; j < HK / 2; j++) {
+                            const float4 f = sv[g * (KT / 2) + j];
+                            // an entry out of sight may hold a NaN scale
+                            const bool v0 = !EDGE || ((vis >> (2 * j)) & 1u), v1 = !EDGE || ((vis >> (2 * j + 1)) & 1u);
+                            P[j] = f2h(v0 ? S[2 * j] * f.x : 0.f, v1 ? S[2 * j + 1] * f.z : 0.f);
                             if (v0) b2[0] = fmaf(S[2 * j], f.y, b2[0]);
                             if (v1) b2[1] = fmaf(S[2 * j + 1], f.w, b2[1]);
-                        } else {
-                            b2[0] = fmaf(S[2 * j], f.y, b2[0]);
-                            b2[1] = fmaf(S[2 * j + 1], f.w, b2[1]);
                         }
-                        P[j] = f2h(e0, e1);
+                        B[g] += b2[0] + b2[1];
+                        const uint32_t at = t_s + g * (KT / 2) + part * (HK / 2);
+                        if (HK == 16) tmem_st8(at, P);
+                        else tmem_st4(at, P);
                     }
-                    B[g] += b2[0] + b2[1];
-                    const uint32_t at = t_s + g * (KT / 2) + half * (HK / 2);
-                    if (HK == 32) tmem_st16(at, *reinterpret_cast<uint32_t(*)[16]>(P));
-                    else tmem_st8(at, P);
-                }
+                };
+                if (edge) store(BoolC<true>{});
+                else store(BoolC<false>{});
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_p[st]);
             }
-            // row sums of both halves, then this half's columns
-            s_sum[half][NG][r] = l;
+            // row sums of the four quarters, then this quarter's columns
+            s_sum[part][NG][r] = l;
 #pragma unroll
-            for (int g = 0; g < NG; g++) s_sum[half][g][r] = B[g];
-            named_bar(1, 256);
+            for (int g = 0; g < NG; g++) s_sum[part][g][r] = B[g];
+            named_bar(1 + q4, 128);
             if (ok) ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(gt + T - 1) & 1], ((gt + T - 1) >> 1) & 1u, c.stop));
             tc_fence_after();
             if (ok) {
-                const float L = s_sum[0][NG][r] + s_sum[1][NG][r];
+                const float L = (s_sum[0][NG][r] + s_sum[1][NG][r]) + (s_sum[2][NG][r] + s_sum[3][NG][r]);
                 const float M = m == -INFINITY ? m : m - unit;
                 const bool whole = u == ie && ib >= blockIdx.x * per;
                 const bool row = rt * kTileRows + r < q.rows;
@@ -415,12 +420,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const float f = L == 0.f ? 0.f : 1.f / L;
                 __half* out = a.out + (size_t)(q.first + rr / G) * a.out_stride + (size_t)head * D;
 #pragma unroll
-                for (int k = 0; k < NG * 2; k++) {
-                    const int col = half * (NG * 32) + k * 16;
+                for (int k = 0; k < NG; k++) {
+                    const int col = part * (NG * 16) + k * 16;
                     uint32_t o[16];
                     tmem_ld16_nw(t_row + Sh::kO + col, o);
                     tmem_ld_wait();
-                    const float bb = s_sum[0][col / 64][r] + s_sum[1][col / 64][r];
+                    const int g = col / 64;
+                    const float bb = (s_sum[0][g][r] + s_sum[1][g][r]) + (s_sum[2][g][r] + s_sum[3][g][r]);
                     if (!row) continue;
                     float v[16];
 #pragma unroll
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
-                if (half == 0 && row) {
+                if (part == 0 && row) {
                     if (whole) {
                         a.lse[(size_t)(q.first + rr / G) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                     } else {
@@ -448,9 +454,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 }
             }
             tc_fence_before();
-        } else if (warp < 12) {
+        } else if (warp < kTileSoft + 4) {
             // --------------------------------------------------- converters --
-            const int ct = tid - 256, cw = warp - 8;
+            const int ct = tid - kTileSoft * 32, cw = warp - kTileSoft;
             const int32_t* trow = c.table + (size_t)s * c.max_pages;
             const int vw = ct & 7, vk = (ct >> 3) % (KT / 8), vg = (ct >> 3) / (KT / 8);   // V: 8 x 8 codes each
             const int eg = ct / KT, ee = ct % KT;                                          // scale and bias of one entry
