@@ -12,6 +12,7 @@
 #include "kv_attn.cuh"
 #include "kv_attn_tc.cuh"
 #include "kv_cache.cuh"
+#include "kv_weights.cuh"
 
 using namespace moeq4;
 
@@ -99,6 +100,16 @@ static TileKernel tile_of() {
 }
 static TileKernel tile_kernel(int ng) {
     static const TileKernel table[4] = {tile_of<1>(), tile_of<2>(), tile_of<3>(), tile_of<4>()};
+    return table[ng - 1];
+}
+typedef void (*WtFn)(const AttnArgs);
+struct WtKernel {
+    WtFn fn;
+    int smem;
+};
+static WtKernel weights_kernel(int ng) {
+    static const WtKernel table[4] = {{k_attn_weights<1>, WtShape<1>::kSmem}, {k_attn_weights<2>, WtShape<2>::kSmem},
+                                      {k_attn_weights<3>, WtShape<3>::kSmem}, {k_attn_weights<4>, WtShape<4>::kSmem}};
     return table[ng - 1];
 }
 static SplitKernel split_kernel(int ng, int rt) {
@@ -189,6 +200,8 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     const size_t o_part = take(part * sizeof(float));
     const size_t o_count = take(ctas * sizeof(int));
     kv->counts = ctas;
+    const WtKernel wt = weights_kernel(cfg->head_dim / 64);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(wt.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, wt.smem);
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
     if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
@@ -351,8 +364,10 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
         KV_CK(kv_launch(split_kernel(a.c.ng, rt).fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads,
                         kv->split_smem[rt - 1], stream, x));
     }
-    if (flags & MOE_ATTN_WEIGHTS)
-        KV_CK(kv_launch(k_attn_weights_simple, dim3(a.c.max_pages, a.c.hkv, a.c.n_seqs), kKvPage, 0, stream, a));
+    if (flags & MOE_ATTN_WEIGHTS) {
+        const WtKernel k = weights_kernel(a.c.ng);
+        KV_CK(kv_launch(k.fn, dim3(2 * kv->n_sms), kWtThreads, k.smem, stream, a));
+    }
     return MOE_OK;
 }
 

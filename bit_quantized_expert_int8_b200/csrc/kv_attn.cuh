@@ -61,6 +61,21 @@ __device__ __forceinline__ uint32_t f2h(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The same pairs as fp16 c - 8.
+__device__ __forceinline__ uint4 codes_centred(uint32_t w) {
+    const uint32_t u = w >> 8;
+    const uint32_t v[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
+                           (u & 0x000F000Fu) | 0x64006400u, (u & 0x00F000F0u) | 0x54005400u};
+    const __half2 o0 = __float2half2_rn(-1032.f), o1 = __float2half2_rn(-72.f);   // -(1024 + 8), -(64 + 8)
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&v[k]), k & 1 ? o1 : o0);
+        r[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -728,42 +743,6 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         }
         __syncthreads();                                     // the ring and s_m are free again
     }
-}
-
-// One element of K (part 0) or V (part 1).
-__device__ __forceinline__ float kv_value(const uint8_t* tile, const KvTile& t, int part, int e, int d) {
-    const int g = d >> 6, c = d & 63;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + t.codes(part, g, e) + (c >> 3) * 4);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(tile + t.sb(part, g, e)));
-    return fmaf(f.x, (float)((w >> (4 * (c & 7))) & 15u), f.y);
-}
-
-// score[s][h][j] += sum over rows and heads of exp(S - lse): one thread per
-// entry.  grid (max_pages, hkv, n_seqs), block 64.
-__global__ void __launch_bounds__(kKvPage) k_attn_weights_simple(const AttnArgs a) {
-    const KvArgs& c = a.c;
-    const int pg = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
-    kv_begin();
-    const int len = kv_len(c, s, false), j = pg * kKvPage + tid;
-    int first;
-    const int n = kv_rows(c, s, &first, false);
-    if (j >= len || n == 0) return;
-    const uint8_t* tile = kv_tile(c, s, pg, h);
-    if (!tile) return;
-    const int D = c.ng * 64, G = c.hq / c.hkv;
-    const KvTile t(c.ng);
-    float sum = 0.f;
-    for (int i = 0; i < n; i++) {
-        const int p = len - n + i;
-        if (j > p || (a.window > 0 && j <= p - a.window)) continue;
-        for (int u = 0; u < G; u++) {
-            const __half* q = a.q + (size_t)(first + i) * a.q_stride + (size_t)(h * G + u) * D;
-            float x = 0.f;
-            for (int d = 0; d < D; d++) x = fmaf(__half2float(q[d]), kv_value(tile, t, 0, tid, d), x);
-            sum += expf(x * a.scale - a.lse[(size_t)(first + i) * c.hq + h * G + u]);
-        }
-    }
-    c.score[((size_t)s * c.hkv + h) * ((size_t)c.max_pages * kKvPage) + j] += sum;
 }
 
 }  // namespace moeq4

@@ -102,21 +102,6 @@ __device__ __forceinline__ TileSeq tile_seq(const TileArgs& x, int s, bool repor
     return q;
 }
 
-// Pairs (i, i + 4) of a word's nibbles as fp16 c - 8.
-__device__ __forceinline__ uint4 codes_centred(uint32_t w) {
-    const uint32_t u = w >> 8;
-    const uint32_t v[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
-                           (u & 0x000F000Fu) | 0x64006400u, (u & 0x00F000F0u) | 0x54005400u};
-    const __half2 o0 = __float2half2_rn(-1032.f), o1 = __float2half2_rn(-72.f);   // -(1024 + 8), -(64 + 8)
-    uint32_t r[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&v[k]), k & 1 ? o1 : o0);
-        r[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 template <int NG>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x) {
     using Sh = TileShape<NG>;
