@@ -48,17 +48,21 @@ static inline bool kv_al(const void* p, uintptr_t n) { return ((uintptr_t)p & (n
 // Launch that may be scheduled before the kernel ahead of it in the stream ends
 // (every kernel here begins with kv_begin, which waits for it).
 template <typename... P, typename... A>
-static cudaError_t kv_launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+static cudaError_t kv_launch(int cluster, void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t lc{};
     lc.gridDim = grid;
     lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     lc.attrs = at;
-    lc.numAttrs = 1;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&lc, fn, static_cast<P>(args)...);
 }
 
@@ -204,7 +208,7 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(wt.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, wt.smem);
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
     if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictSmem);
     if (e != cudaSuccess) {
         const int rc = kv_fail(MOE_ERR_CUDA, "moe_kv_create: %s", cudaGetErrorString(e));
         moe_kv_destroy(kv);
@@ -306,8 +310,9 @@ static int kv_rows_call(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* b
     const KvArgs a = kv_args(kv, cache, batch, batch->n_seqs);
     __half* kp = reinterpret_cast<__half*>(k);
     __half* vp = reinterpret_cast<__half*>(v);
-    KV_CK(kv_launch(read ? k_kv_rows<true> : k_kv_rows<false>, dim3(batch->n_rows), kKvRowThreads, 0, s, a, kp,
-                    k_stride, vp, v_stride));
+    const int64_t jobs = (int64_t)a.n_rows * ((a.hkv * 2 * a.ng + kKvRowGroups - 1) / kKvRowGroups);
+    KV_CK(kv_launch(1, read ? k_kv_rows<true> : k_kv_rows<false>, dim3((unsigned)((jobs + kKvRowWarps - 1) / kKvRowWarps)),
+                    kKvRowThreads, 0, s, a, kp, k_stride, vp, v_stride));
     return MOE_OK;
 }
 
@@ -356,17 +361,17 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     if (tile) {
         TileArgs y{a, kv->part, kv->count, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
         const TileKernel k = tile_kernel(a.c.ng);
-        KV_CK(kv_launch(k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
+        KV_CK(kv_launch(1, k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
     }
     if (!tile || a.c.n_seqs > 1) {
         const int rt = most <= 8 ? 1 : 2;
         SplitArgs x{a, kv->part, kv->count, kSplitMaxRows};
-        KV_CK(kv_launch(split_kernel(a.c.ng, rt).fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads,
+        KV_CK(kv_launch(1, split_kernel(a.c.ng, rt).fn, dim3(kv->split_ctas[rt - 1]), kSplitThreads,
                         kv->split_smem[rt - 1], stream, x));
     }
     if (flags & MOE_ATTN_WEIGHTS) {
         const WtKernel k = weights_kernel(a.c.ng);
-        KV_CK(kv_launch(k.fn, dim3(2 * kv->n_sms), kWtThreads, k.smem, stream, a));
+        KV_CK(kv_launch(1, k.fn, dim3(2 * kv->n_sms), kWtThreads, k.smem, stream, a));
     }
     return MOE_OK;
 }
@@ -385,11 +390,15 @@ extern "C" int moe_kv_evict(moe_kv* kv, const MoeKvCache* cache, int n_seqs, int
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: need 0 <= n_recent <= budget, budget >= 1", who);
     if (new_lens < cache->lens + n_seqs && cache->lens < new_lens + n_seqs)
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: new_lens overlaps lens", who);
-    const size_t smem = evict_smem(kv->cfg.max_pages * kKvPage);
-    if (kv->cfg.max_pages > 8192 || smem > kv->smem_optin)
+    if (kv->cfg.max_pages > 8192)
         return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: max_pages=%d above 8192", who, kv->cfg.max_pages);
     KV_TRY(kv_check_device(kv, who));
     const KvArgs a = kv_args(kv, cache, nullptr, n_seqs);
-    KV_CK(kv_launch(k_kv_evict, dim3(a.hkv, n_seqs), kEvictThreads, smem, stream, a, budget, n_recent, new_lens));
+    // clusters: what fits the device at once (two CTAs per SM), parts of 2048 entries at least
+    const int cap = kv->cfg.max_pages * kKvPage;
+    int parts = 1;
+    while (parts < 8 && (int64_t)n_seqs * a.hkv * parts * 2 <= 2 * kv->n_sms && cap / (parts * 2) >= 2048) parts *= 2;
+    KV_CK(kv_launch(parts, k_kv_evict, dim3(a.hkv * parts, n_seqs), kEvictThreads, evict_smem(evict_part(cap, parts)), stream,
+                    a, budget, n_recent, new_lens));
     return MOE_OK;
 }

@@ -1,6 +1,8 @@
 // kv_cache.cuh -- the 4-bit KV cache: page layout, appending and reading rows,
 // eviction by accumulated attention weight.  Layout and rules in moeq4.h.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -58,17 +60,6 @@ __device__ __forceinline__ int kv_rows(const KvArgs& a, int s, int* first, bool 
     return 0;
 }
 
-// Tile of (sequence s, page slot p, kv head h), or null where the page index
-// is outside the pool.
-__device__ __forceinline__ uint8_t* kv_tile(const KvArgs& a, int s, int p, int h) {
-    const int pg = a.table[(size_t)s * a.max_pages + p];
-    if ((unsigned)pg >= (unsigned)a.n_pages) {
-        kv_flag(a.status);
-        return nullptr;
-    }
-    return a.pages + ((size_t)pg * a.hkv + h) * (size_t)(4608 * a.ng);
-}
-
 // Sequence that owns row r: the count of row_start[1..n] at most r, taken by a
 // whole warp with independent loads (a binary search would chain its loads).
 __device__ __forceinline__ int kv_seq_of_row(const KvArgs& a, int r) {
@@ -79,102 +70,135 @@ __device__ __forceinline__ int kv_seq_of_row(const KvArgs& a, int r) {
 }
 
 // ------------------------------------------------------ append and read --
-// One block per row; eight lanes per group of 64 columns, one 16-byte load
-// and one code word each.  READ turns the direction round.
-constexpr int kKvRowThreads = 256;
+// A warp takes 32 groups of 64 columns of one row (kv heads x K, V x groups):
+// eight lanes a group, four groups at once, eight times over with every load in
+// flight before the first is used; an append loads its row while it still looks
+// for the row's place (sequence, length, page: three dependent reads).  Bound by
+// memory: 128 bytes a group on the fp16 side, 36 on the other.
+constexpr int kKvRowWarps = 4;
+constexpr int kKvRowThreads = kKvRowWarps * 32;
+constexpr int kKvRowGroups = 32;
 
 template <bool READ>
 __global__ void __launch_bounds__(kKvRowThreads)
 k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_stride) {
-    const int r = blockIdx.x;
+    constexpr int N = kKvRowGroups / 4;
+    const int lane = threadIdx.x & 31, w = lane & 7;
+    const int items = a.hkv * 2 * a.ng, chunks = (items + kKvRowGroups - 1) / kKvRowGroups;
+    const long long job = (long long)blockIdx.x * kKvRowWarps + (threadIdx.x >> 5);
     kv_begin();
+    const int r = (int)(job / chunks), it0 = (int)(job % chunks) * kKvRowGroups + (lane >> 3);
+    if (r >= a.n_rows) return;
+    const int per = a.hkv * a.ng;                                // groups of K, then of V
+    const auto row = [&](int it) {
+        const bool is_v = it >= per;
+        const int hg = is_v ? it - per : it;
+        return reinterpret_cast<uint4*>((is_v ? v + (size_t)r * v_stride : k + (size_t)r * k_stride) + (size_t)hg * 64) + w;
+    };
+    uint4 in[N];
+    if (!READ) {
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            in[n] = make_uint4(0, 0, 0, 0);
+            if (it0 + 4 * n < items) in[n] = *row(it0 + 4 * n);
+        }
+    }
     const int s = kv_seq_of_row(a, r);
     if (s >= a.n_seqs) return;                                  // behind the last sequence
     int first;
-    const int n = kv_rows(a, s, &first, threadIdx.x == 0);
+    const bool tell = job % chunks == 0 && lane == 0;
+    const int n = kv_rows(a, s, &first, tell);
     const int i = r - first;
     if (i < 0 || i >= n) return;
-    const int e = kv_len(a, s, threadIdx.x == 0) - n + i;
+    const int e = kv_len(a, s, tell) - n + i;
     if (e < 0) {
-        if (threadIdx.x == 0) kv_flag(a.status);
+        if (tell) kv_flag(a.status);
         return;
     }
     const KvTile t(a.ng);
     const int pg = a.table[(size_t)s * a.max_pages + e / kKvPage];
     if ((unsigned)pg >= (unsigned)a.n_pages) {
-        if (threadIdx.x == 0) kv_flag(a.status);
+        if (tell) kv_flag(a.status);
         return;
     }
+    const int en = e % kKvPage;
     uint8_t* page = a.pages + (size_t)pg * a.hkv * t.bytes();
-    const int en = e % kKvPage, w = threadIdx.x & 7;
-    const int items = a.hkv * 2 * a.ng;
-    for (int base = 0; base < items; base += kKvRowThreads / 8) {
-        const int it = base + (threadIdx.x >> 3);
-        const bool on = it < items;
-        const int part = on ? it / (a.hkv * a.ng) : 0, hg = on ? it % (a.hkv * a.ng) : 0;
-        const int h = hg / a.ng, g = hg % a.ng;
+    const auto codes = [&](int it) {                            // this lane's code word, and the group's scale
+        const int part = it >= per, hg = part ? it - per : it, h = hg / a.ng, g = hg - h * a.ng;
         uint8_t* tile = page + (size_t)h * t.bytes();
-        uint32_t* cw = reinterpret_cast<uint32_t*>(tile + t.codes(part, g, en)) + w;
-        __half2* sb = reinterpret_cast<__half2*>(tile + t.sb(part, g, en));
-        uint4* x = reinterpret_cast<uint4*>((part ? v + (size_t)r * v_stride : k + (size_t)r * k_stride) +
-                                            (size_t)h * a.ng * 64 + g * 64) + w;
-        if (READ) {
-            if (!on) continue;
-            const float2 f = __half22float2(*sb);
-            const uint32_t c = *cw;
+        return make_ulonglong2((unsigned long long)(reinterpret_cast<uint32_t*>(tile + t.codes(part, g, en)) + w),
+                               (unsigned long long)(tile + t.sb(part, g, en)));
+    };
+    if (READ) {
+        uint32_t cw[N], sb[N];
+#pragma unroll
+        for (int q = 0; q < N; q++) {
+            if (it0 + 4 * q >= items) continue;
+            const ulonglong2 at = codes(it0 + 4 * q);
+            cw[q] = *reinterpret_cast<const uint32_t*>(at.x);
+            sb[q] = *reinterpret_cast<const uint32_t*>(at.y);
+        }
+#pragma unroll
+        for (int q = 0; q < N; q++) {
+            if (it0 + 4 * q >= items) continue;
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sb[q]));
             uint4 o;
             uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const __half2 p = __floats2half2_rn(fmaf(f.x, (float)((c >> (8 * q)) & 15u), f.y),
-                                                    fmaf(f.x, (float)((c >> (8 * q + 4)) & 15u), f.y));
-                ow[q] = *reinterpret_cast<const uint32_t*>(&p);
+            for (int c = 0; c < 4; c++) {
+                const __half2 p = __floats2half2_rn(fmaf(f.x, (float)((cw[q] >> (8 * c)) & 15u), f.y),
+                                                    fmaf(f.x, (float)((cw[q] >> (8 * c + 4)) & 15u), f.y));
+                ow[c] = *reinterpret_cast<const uint32_t*>(&p);
             }
-            *x = o;
-        } else {
-            const uint4 in = on ? *x : make_uint4(0, 0, 0, 0);
-            const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
-            float f[8];
-            bool fin = true;
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&iw[q]));
-                f[2 * q] = p.x;
-                f[2 * q + 1] = p.y;
-                fin = fin && fabsf(p.x) <= 65504.f && fabsf(p.y) <= 65504.f;   // false for NaN
-            }
-            float lo = f[0], hi = f[0];
-#pragma unroll
-            for (int q = 1; q < 8; q++) {
-                lo = fminf(lo, f[q]);
-                hi = fmaxf(hi, f[q]);
-            }
-            int bad = fin ? 0 : 1;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-            }
-            if (!on) continue;
-            const __half sc = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
-            const __half bi = __float2half_rn(lo);
-            const float sf = __half2float(sc), bf = __half2float(bi);
-            uint32_t c = 0;
-            if (!bad && sf != 0.f) {
-#pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    const float u = rintf(__fdiv_rn(f[q] - bf, sf));
-                    c |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * q);
-                }
-            }
-            *cw = c;
-            if (w == 0) *sb = bad ? __halves2half2(__ushort_as_half(0x7FFF), __ushort_as_half(0x7FFF))
-                                  : __halves2half2(sc, bi);
+            *row(it0 + 4 * q) = o;
         }
+        return;
     }
-    if (!READ)
-        for (int h = threadIdx.x; h < a.hkv; h += kKvRowThreads) {
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+        const uint32_t iw[4] = {in[q].x, in[q].y, in[q].z, in[q].w};
+        float f[8];
+        bool fin = true;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&iw[c]));
+            f[2 * c] = p.x;
+            f[2 * c + 1] = p.y;
+            fin = fin && fabsf(p.x) <= 65504.f && fabsf(p.y) <= 65504.f;       // false for NaN
+        }
+        float lo = f[0], hi = f[0];
+#pragma unroll
+        for (int c = 1; c < 8; c++) {
+            lo = fminf(lo, f[c]);
+            hi = fmaxf(hi, f[c]);
+        }
+        int bad = fin ? 0 : 1;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        }
+        if (it0 + 4 * q >= items) continue;
+        const __half sc = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
+        const __half bi = __float2half_rn(lo);
+        const float sf = __half2float(sc), bf = __half2float(bi);
+        uint32_t c = 0;
+        if (!bad && sf != 0.f) {
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+                const float u = rintf(__fdiv_rn(f[x] - bf, sf));
+                c |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * x);
+            }
+        }
+        const ulonglong2 at = codes(it0 + 4 * q);
+        *reinterpret_cast<uint32_t*>(at.x) = c;
+        if (w == 0)
+            *reinterpret_cast<__half2*>(at.y) = bad ? __halves2half2(__ushort_as_half(0x7FFF), __ushort_as_half(0x7FFF))
+                                                    : __halves2half2(sc, bi);
+    }
+    if (job % chunks == 0)
+        for (int h = lane; h < a.hkv; h += 32) {
             const size_t at = ((size_t)s * a.hkv + h) * ((size_t)a.max_pages * kKvPage) + e;
             if (a.score) a.score[at] = 0.f;
             if (a.pos) a.pos[at] = a.seen[s] - n + i;
@@ -182,14 +206,19 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
 }
 
 // -------------------------------------------------------------- eviction --
-// One block per (kv head, sequence).  The budget-th largest rank of the
-// entries is found by a radix selection on an order-preserving 32-bit key
-// (11 + 11 + 10 bits, one histogram pass each); a bit per entry then says
-// whether it stays.  The r-th staying entry behind the budget moves into the
-// r-th free place below it; both are found through prefix counts over the
-// words of bits, so no list leaves shared memory.
-constexpr int kEvictThreads = 1024;
+// One cluster of CTAs per (kv head, sequence), each with an equal part of the
+// entries.  The budget-th largest rank is found by a radix selection on an
+// order-preserving 32-bit key (11 + 11 + 10 bits): every CTA counts its part,
+// the counts meet in the cluster's first CTA through distributed shared memory,
+// which finds the threshold.  A bit per entry then says whether it stays.  The r-th staying entry
+// behind the budget moves into the r-th free place below it; both are found by a
+// search in prefix counts over the words of bits, wherever in the cluster they
+// lie, so the ranks (and with them the copying) are shared evenly and no list
+// leaves shared memory.  The clusters are as large as fills the device (a cluster
+// per pair alone leaves most SMs idle when there are few pairs).
+constexpr int kEvictThreads = 512;
 constexpr int kEvictBins = 2048;
+constexpr int kEvictKeys = 16384;      // entries of a part whose keys are kept in shared memory
 
 // Rank of an entry: last tokens above all, then by score; NaN below all.
 __device__ __forceinline__ uint32_t evict_key(float score, bool recent) {
@@ -199,12 +228,21 @@ __device__ __forceinline__ uint32_t evict_key(float score, bool recent) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// words of bits, prefix counts, histogram, scan scratch
-__host__ __device__ constexpr size_t evict_smem(int cap) {
-    return (size_t)((cap + 31) / 32) * 8 + kEvictBins * 4 + 64 * 4;
+// Entries of one CTA at most, for a cluster of `parts`.
+__host__ __device__ constexpr int evict_part(int cap, int parts) { return ((cap + parts - 1) / parts + 31) / 32 * 32; }
+// bits, prefix counts, histogram, moves, and the keys of a part where they fit
+__host__ __device__ constexpr size_t evict_smem(int part) {
+    return (size_t)(part / 32) * 4 + (size_t)(part / 32 + 2) * 4 + kEvictBins * 4 + kEvictThreads * 16 +
+           (part <= kEvictKeys ? (size_t)part * 4 : 0);
 }
 
+// The most that a part of 524288 entries (max_pages 8192) asks for, alone or in a
+// cluster: without keys beyond kEvictKeys, with them up to there.
+constexpr int kEvictSmem = 148 * 1024;
+static_assert(evict_smem(524288) <= kEvictSmem && evict_smem(kEvictKeys) <= kEvictSmem, "eviction's shared memory");
+
 __device__ __forceinline__ int block_exclusive_scan(int v, int* s_scan, int* total) {
+    constexpr int W = kEvictThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -215,146 +253,231 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* s_scan, int* tot
     __syncthreads();
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int t = s_scan[lane];
+    int before = 0, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
-        }
-        s_scan[lane] = t;
+    for (int w = 0; w < W; w++) {
+        const int t = s_scan[w];
+        before += w < warp ? t : 0;
+        all += t;
     }
-    __syncthreads();
-    *total = s_scan[kEvictThreads / 32 - 1];
-    return x - v + (warp ? s_scan[warp - 1] : 0);
+    *total = all;
+    return x - v + before;
+}
+
+// What stays in word w of a part that begins at entry e0: free places below the
+// budget, and entries to move at or behind it.
+__device__ __forceinline__ uint32_t evict_holes(uint32_t bits, int lo, int budget) {
+    if (lo >= budget) return 0u;
+    return ~bits & (budget - lo >= 32 ? 0xFFFFFFFFu : (1u << (budget - lo)) - 1u);
+}
+__device__ __forceinline__ uint32_t evict_movers(uint32_t bits, int lo, int budget) {
+    if (lo + 32 <= budget) return 0u;
+    return bits & (lo >= budget ? 0xFFFFFFFFu : ~((1u << (budget - lo)) - 1u));
 }
 
 __global__ void __launch_bounds__(kEvictThreads)
 k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_lens) {
+    namespace cg = cooperative_groups;
     extern __shared__ __align__(16) uint32_t ev_smem[];
-    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+    __shared__ int s_scan[kEvictThreads / 32], s_res[2], s_cnt[3], s_hc[8], s_mc[8];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+    const int h = blockIdx.x / C, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const int cap = a.max_pages * kKvPage;
     kv_begin();
-    const int len = kv_len(a, s, h == 0 && tid == 0);
-    if (h == 0 && tid == 0) new_lens[s] = min(len, budget);
-    if (len <= budget) return;
-    const int words = (len + 31) / 32;
-    uint32_t* bits = ev_smem;
-    uint32_t* pre = bits + (cap + 31) / 32;
-    uint32_t* hist = pre + (cap + 31) / 32;
-    int* s_scan = reinterpret_cast<int*>(hist + kEvictBins);   // 32 words, then 2 of results
-    int* s_res = s_scan + 32;
+    const bool first = h == 0 && me == 0 && tid == 0;
+    const int len = kv_len(a, s, first);
+    if (first) new_lens[s] = min(len, budget);
+    if (len <= budget) return;                                  // the whole cluster alike
+    const int part_cap = evict_part(cap, C);
+    uint32_t* hist = ev_smem;
+    int4* list = reinterpret_cast<int4*>(hist + kEvictBins);    // from, to, their pages
+    uint32_t* bits = reinterpret_cast<uint32_t*>(list + kEvictThreads);
+    uint32_t* pre = bits + part_cap / 32;
+    uint32_t* keys = pre + part_cap / 32 + 2;
+    const bool kept = part_cap <= kEvictKeys;
     const size_t at = ((size_t)s * a.hkv + h) * (size_t)cap;
     float* score = a.score + at;
     int32_t* pos = a.pos + at;
     const int since = a.seen[s] - n_recent;
+    const int part = evict_part(len, C);
+    const int e0 = min(me * part, len), n = min(len - e0, part), words = (n + 31) / 32;
+    const auto key_of = [&](int i) { return evict_key(score[e0 + i], pos[e0 + i] >= since); };
+    if (kept)
+        for (int i = tid; i < n; i += kEvictThreads) keys[i] = key_of(i);
 
     // the budget-th largest key T, and how many entries equal to T stay
     uint32_t prefix = 0, mask = 0;
     int need = budget;
     for (int pass = 0; pass < 3; pass++) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const int nb = pass == 2 ? 1024 : 2048;
+        const uint32_t low = pass == 2 ? 1023u : 2047u;
         for (int b = tid; b < kEvictBins; b += kEvictThreads) hist[b] = 0;
         __syncthreads();
-        for (int e = tid; e < len; e += kEvictThreads) {
-            const uint32_t key = evict_key(score[e], pos[e] >= since);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (nb - 1)], 1u);
+        for (int i = tid; i < n; i += kEvictThreads) {
+            const uint32_t key = kept ? keys[i] : key_of(i);
+            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & low], 1u);
         }
         __syncthreads();
-        // bins from the top, two per thread
-        const int b1 = kEvictBins - 1 - 2 * tid, b0 = b1 - 1;
-        const int c1 = (int)hist[b1], c0 = (int)hist[b0];
-        int total;
-        const int above = block_exclusive_scan(c0 + c1, s_scan, &total);
-        if (above < need && need <= above + c1) { s_res[0] = b1; s_res[1] = need - above; }
-        else if (above + c1 < need && need <= above + c1 + c0) { s_res[0] = b0; s_res[1] = need - above - c1; }
-        __syncthreads();
-        prefix |= (uint32_t)s_res[0] << shift;
-        mask |= (uint32_t)(nb - 1) << shift;
-        need = s_res[1];
-        __syncthreads();
+        if (C > 1) {                                            // the parts' counts meet in the first CTA
+            cluster.sync();
+            uint32_t* h0 = cluster.map_shared_rank(hist, 0);
+            for (int b = tid; me > 0 && b < kEvictBins; b += kEvictThreads)
+                if (hist[b]) atomicAdd(h0 + b, hist[b]);
+            cluster.sync();
+        }
+        if (me == 0) {                                          // four bins per thread, from the top
+            constexpr int B = kEvictBins / kEvictThreads;
+            const int top = kEvictBins - 1 - B * tid;
+            int cnt[B], sum = 0, total;
+#pragma unroll
+            for (int k = 0; k < B; k++) sum += cnt[k] = (int)hist[top - k];
+            int above = block_exclusive_scan(sum, s_scan, &total);
+#pragma unroll
+            for (int k = 0; k < B; k++) {
+                if (above < need && need <= above + cnt[k]) {
+                    s_res[0] = top - k;
+                    s_res[1] = need - above;
+                }
+                above += cnt[k];
+            }
+        }
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        const int* res = cluster.map_shared_rank(s_res, 0);
+        prefix |= (uint32_t)res[0] << shift;
+        mask |= low << shift;
+        need = res[1];
     }
-    // ties at T stay in index order: count them per word first
-    const int lane = tid & 31;
+    // ties at T stay in index order
     for (int w = tid >> 5; w < words; w += kEvictThreads / 32) {
-        const int e = w * 32 + lane;
-        const uint32_t key = e < len ? evict_key(score[e], pos[e] >= since) : 0u;
-        const uint32_t up = __ballot_sync(0xffffffffu, e < len && key > prefix);
-        const uint32_t eq = __ballot_sync(0xffffffffu, e < len && key == prefix);
+        const int i = w * 32 + lane;
+        const uint32_t key = i < n ? (kept ? keys[i] : key_of(i)) : 0u;
+        const uint32_t up = __ballot_sync(0xffffffffu, i < n && key > prefix);
+        const uint32_t eq = __ballot_sync(0xffffffffu, i < n && key == prefix);
         if (lane == 0) { bits[w] = up; pre[w] = eq; }
     }
     __syncthreads();
     const int per = (words + kEvictThreads - 1) / kEvictThreads;
     const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
-    int n = 0, total;
-    for (int w = w0; w < w1; w++) n += __popc(pre[w]);
-    int left = need - block_exclusive_scan(n, s_scan, &total);
+    int ties = 0, all;
+    for (int w = w0; w < w1; w++) ties += __popc(pre[w]);
+    const int mine = block_exclusive_scan(ties, s_scan, &all);
+    if (tid == 0) s_cnt[0] = all;
+    cluster.sync();
+    int left = need - mine;
+    for (int r = 0; r < me; r++) left -= *cluster.map_shared_rank(&s_cnt[0], r);
     for (int w = w0; w < w1; w++) {
         uint32_t eq = pre[w], take = 0;
-        while (eq && left > 0) {
-            const uint32_t low = eq & (0u - eq);
-            take |= low;
-            eq ^= low;
-            left--;
+        if (__popc(eq) <= left) {
+            take = eq;
+            left -= __popc(eq);
+        }
+        for (; take != eq && left > 0; left--) {
+            const uint32_t lowest = (eq & ~take) & (0u - (eq & ~take));
+            take |= lowest;
         }
         bits[w] |= take;
     }
-    __syncthreads();
-    // free places below the budget (bit 0 there), entries to move at or behind it
-    // (bit 1 there): word-wise counts, free places first in the low half
-    const auto holes = [&](int w) -> uint32_t {
-        const int lo = w * 32;
-        if (lo >= budget) return 0u;
-        const uint32_t in = budget - lo >= 32 ? 0xFFFFFFFFu : (1u << (budget - lo)) - 1u;
-        return ~bits[w] & in;
-    };
-    const auto movers = [&](int w) -> uint32_t {
-        const int lo = w * 32;
-        if (lo + 32 <= budget) return 0u;
-        const uint32_t out = lo >= budget ? 0xFFFFFFFFu : ~((1u << (budget - lo)) - 1u);
-        return bits[w] & out;
-    };
+    // prefix counts: free places at pre[w], entries to move at pre[w + 1] (a word below the
+    // budget has none to move, one behind it no free place, so the two never meet)
     int nh = 0, nm = 0, th, tm;
-    for (int w = w0; w < w1; w++) { nh += __popc(holes(w)); nm += __popc(movers(w)); }
-    int ph = block_exclusive_scan(nh, s_scan, &th);
-    const int pm = block_exclusive_scan(nm, s_scan, &tm);
-    for (int w = w0; w < w1; w++) { pre[w] = (uint32_t)ph; ph += __popc(holes(w)); }
-    __syncthreads();
-    const KvTile t(a.ng);
-    int rank = pm;
-    const int bw = (budget + 31) / 32;                          // words that hold free places
     for (int w = w0; w < w1; w++) {
-        uint32_t m = movers(w);
-        while (m) {
-            const int src = w * 32 + __ffs(m) - 1;
-            m &= m - 1;
-            int lo = 0, hi = bw - 1;                            // last word with pre <= rank
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if ((int)pre[mid] <= rank) lo = mid;
-                else hi = mid - 1;
-            }
-            uint32_t f = holes(lo);
-            for (int q = rank - (int)pre[lo]; q > 0; q--) f &= f - 1;
-            const int dst = lo * 32 + __ffs(f) - 1;
-            rank++;
-            score[dst] = score[src];
-            pos[dst] = pos[src];
-            const uint8_t* ts = kv_tile(a, s, src / kKvPage, h);
-            uint8_t* td = kv_tile(a, s, dst / kKvPage, h);
-            if (!ts || !td) continue;
-            for (int part = 0; part < 2; part++)
-                for (int g = 0; g < a.ng; g++) {
-                    const uint4* cs = reinterpret_cast<const uint4*>(ts + t.codes(part, g, src % kKvPage));
-                    uint4* cd = reinterpret_cast<uint4*>(td + t.codes(part, g, dst % kKvPage));
-                    cd[0] = cs[0];
-                    cd[1] = cs[1];
-                    *reinterpret_cast<uint32_t*>(td + t.sb(part, g, dst % kKvPage)) =
-                        *reinterpret_cast<const uint32_t*>(ts + t.sb(part, g, src % kKvPage));
-                }
-        }
+        nh += __popc(evict_holes(bits[w], e0 + w * 32, budget));
+        nm += __popc(evict_movers(bits[w], e0 + w * 32, budget));
     }
+    int ph = block_exclusive_scan(nh, s_scan, &th);             // (its barriers: pre has been read)
+    int pm = block_exclusive_scan(nm, s_scan, &tm);
+    for (int w = w0; w < w1; w++) {
+        const int lo = e0 + w * 32;
+        if (lo < budget) pre[w] = (uint32_t)ph;
+        if (lo + 32 > budget) pre[w + 1] = (uint32_t)pm;
+        ph += __popc(evict_holes(bits[w], lo, budget));
+        pm += __popc(evict_movers(bits[w], lo, budget));
+    }
+    if (tid == 0) { s_cnt[1] = th; s_cnt[2] = tm; }
+    cluster.sync();
+    if (tid < C) {
+        s_hc[tid] = *cluster.map_shared_rank(&s_cnt[1], tid);
+        s_mc[tid] = *cluster.map_shared_rank(&s_cnt[2], tid);
+    }
+    __syncthreads();
+    int moves = 0;
+    for (int r = 0; r < C; r++) moves += s_mc[r];
+    const int r0 = (int)((long long)moves * me / C), r1 = (int)((long long)moves * (me + 1) / C);
+    // the entry with rank k among free places (or entries to move) of the cluster
+    const auto find = [&](int k, const int* count, bool hole) {
+        int r = 0;
+        while (k >= count[r]) k -= count[r++];
+        const uint32_t* br = cluster.map_shared_rank(bits, r);
+        const uint32_t* pr = cluster.map_shared_rank(pre, r) + (hole ? 0 : 1);
+        const int b = r * part, nw = (min(len - b, part) + 31) / 32;
+        int lo = hole ? 0 : max(0, (budget - b) / 32), hi = (hole ? min(nw, (budget - b + 31) / 32) : nw) - 1;
+        while (lo < hi) {                                       // last word with prefix <= k
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int)pr[mid] <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        uint32_t f = hole ? evict_holes(br[lo], b + lo * 32, budget) : evict_movers(br[lo], b + lo * 32, budget);
+        for (int q = k - (int)pr[lo]; q > 0; q--) f &= f - 1;
+        return b + lo * 32 + __ffs(f) - 1;
+    };
+    const KvTile t(a.ng);
+    // 2^sh lanes a move: 4 ng of them copy 16 bytes of codes, 2 ng a scale and bias, two the
+    // score and the position; four moves a lane in flight
+    const int sh = a.ng == 1 ? 3 : a.ng == 2 ? 4 : 5, p = tid & ((1 << sh) - 1);
+    size_t unit = 0;                                            // this lane's bytes in a tile, and per entry
+    int off = 0, step = 32;
+    if (p < 4 * a.ng) {
+        off = t.codes(p / (2 * a.ng), (p >> 1) % a.ng, 0) + (p & 1) * 16;
+    } else if (p < 6 * a.ng) {
+        off = t.sb((p - 4 * a.ng) / a.ng, (p - 4 * a.ng) % a.ng, 0);
+        step = 4;
+    }
+    unit = (size_t)h * t.bytes() + off;
+    const size_t page_bytes = (size_t)a.hkv * t.bytes();
+    const int32_t* trow = a.table + (size_t)s * a.max_pages;
+    for (int k0 = r0; k0 < r1; k0 += kEvictThreads) {
+        const int m = min(kEvictThreads, r1 - k0);
+        if (tid < m) {
+            const int from = find(k0 + tid, s_mc, false), to = find(k0 + tid, s_hc, true);
+            int2 pg = make_int2(trow[from / kKvPage], trow[to / kKvPage]);
+            if ((unsigned)pg.x >= (unsigned)a.n_pages || (unsigned)pg.y >= (unsigned)a.n_pages) {
+                kv_flag(a.status);
+                pg.x = -1;
+            }
+            list[tid] = make_int4(from, to, pg.x, pg.y);
+        }
+        __syncthreads();
+        const int each = kEvictThreads >> sh;                   // moves in flight in a step
+        for (int i0 = tid >> sh; i0 < m; i0 += 4 * each) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int i = i0 + k * each;
+                if (i >= m) continue;
+                const int4 e = list[i];
+                const uint8_t* src = a.pages + (size_t)e.z * page_bytes + unit + (e.x % kKvPage) * step;
+                if (p < 4 * a.ng) { if (e.z >= 0) v[k] = *reinterpret_cast<const uint4*>(src); }
+                else if (p < 6 * a.ng) { if (e.z >= 0) v[k].x = *reinterpret_cast<const uint32_t*>(src); }
+                else if (p == 6 * a.ng) v[k].x = __float_as_uint(score[e.x]);
+                else if (p == 6 * a.ng + 1) v[k].x = (uint32_t)pos[e.x];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int i = i0 + k * each;
+                if (i >= m) continue;
+                const int4 e = list[i];
+                uint8_t* dst = a.pages + (size_t)e.w * page_bytes + unit + (e.y % kKvPage) * step;
+                if (p < 4 * a.ng) { if (e.z >= 0) *reinterpret_cast<uint4*>(dst) = v[k]; }
+                else if (p < 6 * a.ng) { if (e.z >= 0) *reinterpret_cast<uint32_t*>(dst) = v[k].x; }
+                else if (p == 6 * a.ng) score[e.y] = __uint_as_float(v[k].x);
+                else if (p == 6 * a.ng + 1) pos[e.y] = (int)v[k].x;
+            }
+        }
+        __syncthreads();
+    }
+    cluster.sync();                                             // no CTA leaves while its bits are read
 }
 
 }  // namespace moeq4
