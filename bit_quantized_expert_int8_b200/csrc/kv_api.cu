@@ -310,9 +310,13 @@ static int kv_rows_call(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* b
     const KvArgs a = kv_args(kv, cache, batch, batch->n_seqs);
     __half* kp = reinterpret_cast<__half*>(k);
     __half* vp = reinterpret_cast<__half*>(v);
-    const int64_t jobs = (int64_t)a.n_rows * ((a.hkv * 2 * a.ng + kKvRowGroups - 1) / kKvRowGroups);
-    KV_CK(kv_launch(1, read ? k_kv_rows<true> : k_kv_rows<false>, dim3((unsigned)((jobs + kKvRowWarps - 1) / kKvRowWarps)),
-                    kKvRowThreads, 0, s, a, kp, k_stride, vp, v_stride));
+    // 32 groups a warp where that still gives every SM 16 warps, else 4
+    const int items = a.hkv * 2 * a.ng;
+    const bool many = (int64_t)a.n_rows * ((items + 31) / 32) >= 16 * kv->n_sms;
+    const int64_t jobs = (int64_t)a.n_rows * (many ? (items + 31) / 32 : (items + 3) / 4);
+    const auto fn = read ? (many ? k_kv_rows<true, 8> : k_kv_rows<true, 1>) : many ? k_kv_rows<false, 8> : k_kv_rows<false, 1>;
+    KV_CK(kv_launch(1, fn, dim3((unsigned)((jobs + kKvRowWarps - 1) / kKvRowWarps)), kKvRowThreads, 0, s, a, kp, k_stride, vp,
+                    v_stride));
     return MOE_OK;
 }
 

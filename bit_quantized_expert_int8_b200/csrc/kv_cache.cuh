@@ -70,19 +70,19 @@ __device__ __forceinline__ int kv_seq_of_row(const KvArgs& a, int r) {
 }
 
 // ------------------------------------------------------ append and read --
-// A warp takes 32 groups of 64 columns of one row (kv heads x K, V x groups):
-// eight lanes a group, four groups at once, eight times over with every load in
+// A warp takes 4 N groups of 64 columns of one row (kv heads x K, V x groups):
+// eight lanes a group, four groups at once, N times over with every load in
 // flight before the first is used; an append loads its row while it still looks
 // for the row's place (sequence, length, page: three dependent reads).  Bound by
-// memory: 128 bytes a group on the fp16 side, 36 on the other.
+// memory (128 bytes a group on the fp16 side, 36 on the other) with many rows, by
+// that chain with few: then N = 1 spreads a row over as many warps as it has.
 constexpr int kKvRowWarps = 4;
 constexpr int kKvRowThreads = kKvRowWarps * 32;
-constexpr int kKvRowGroups = 32;
 
-template <bool READ>
+template <bool READ, int N>
 __global__ void __launch_bounds__(kKvRowThreads)
 k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_stride) {
-    constexpr int N = kKvRowGroups / 4;
+    constexpr int kKvRowGroups = 4 * N;
     const int lane = threadIdx.x & 31, w = lane & 7;
     const int items = a.hkv * 2 * a.ng, chunks = (items + kKvRowGroups - 1) / kKvRowGroups;
     const long long job = (long long)blockIdx.x * kKvRowWarps + (threadIdx.x >> 5);
@@ -185,9 +185,13 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
         const float sf = __half2float(sc), bf = __half2float(bi);
         uint32_t c = 0;
         if (!bad && sf != 0.f) {
+            // the correctly rounded quotient from the correctly rounded reciprocal and one
+            // corrected step (P. Markstein, IBM J. Res. Dev. 34 (1990), theorem on division)
+            const float rs = __frcp_rn(sf);
 #pragma unroll
             for (int x = 0; x < 8; x++) {
-                const float u = rintf(__fdiv_rn(f[x] - bf, sf));
+                const float d = f[x] - bf, q0 = d * rs;
+                const float u = rintf(fmaf(fmaf(-q0, sf, d), rs, q0));
                 c |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * x);
             }
         }

@@ -386,6 +386,38 @@ def test_append_and_read(D, Hkv, lens, rows):
     assert (ko[n:] == 7).all() and (vo[:, Hkv:] == 7).all() and (vo[n:] == 7).all()
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_append_many_values(seed):
+    """Scales over fp16's whole range, and groups built on half steps: the codes
+    are those of the correctly rounded fp32 quotient, bit for bit."""
+    c = Case(45 + seed, 128, 8, 8, [1500], [1500])
+    rng = c.rng
+    if seed < 2:
+        kv = rng.standard_normal((2, 1500, 8, 128)) * np.exp2(rng.integers(-14, 11, (2, 1500, 8, 1)))
+        if seed:
+            kv = kv + np.exp2(rng.integers(-6, 12, (2, 1500, 8, 1))) * rng.standard_normal((2, 1500, 8, 1))
+        kv = kv.clip(-65504, 65504).astype(np.float16)
+    else:                                              # lo + s (code / 2): quotients at and next to .5
+        s = rng.integers(1024, 2048, (2, 1500, 8, 2, 1)) * np.exp2(rng.integers(-12, -8, (2, 1500, 8, 2, 1)))
+        x = rng.integers(0, 31, (2, 1500, 8, 2, 64)) * 0.5
+        x[..., 0], x[..., 1] = 0, 15
+        lo = 0 if seed == 2 else rng.integers(-2048, 2048, (2, 1500, 8, 2, 1))
+        kv = (lo + s * x).astype(np.float16).reshape(2, 1500, 8, 128)
+    moe_k, moe_v = cu(kv[0]), cu(kv[1])
+    moeq4.moe_kv_append_q4(c.kv, c.cache, c.batch, moe_k, moe_v)
+    moeq4.moe_kv_check(c.kv)
+    got = c.g["pages"].cpu().numpy()[c.table[0]]       # [pages][8][tile]
+    for part in (0, 1):
+        codes, sb = kv_ref.quantise(kv[part].reshape(1500, 8, 2, 64))
+        pad = np.zeros((24 * 64 - 1500, 8, 2, 36), np.uint8)
+        want = np.concatenate((np.concatenate((codes, sb), -1), pad)).reshape(24, 64, 8, 2, 36).transpose(0, 2, 3, 1, 4)
+        o = part * 4608
+        have = np.concatenate((got[:, :, o:o + 4096].reshape(24, 8, 2, 64, 32),
+                               got[:, :, o + 4096:o + 4608].reshape(24, 8, 2, 64, 4)), -1)
+        have[-1, :, :, 1500 - 23 * 64:] = 0
+        assert np.array_equal(have, want)
+
+
 # --------------------------------------------------------------- eviction --
 def check_evict(c, budget, recent):
     new = torch.full((c.n,), -5, dtype=torch.int32, device=DEV)
