@@ -80,6 +80,7 @@ struct moe_kv {
     int split_smem[2] = {0, 0};
     int tile_smem = 0;         // of the tile kernel; 0 where no call can have enough rows for it
     size_t counts = 0;         // length of count
+    TileCut* cut = nullptr;    // [n_sms]
 };
 
 // The split kernel of one head size and row-tile count.
@@ -95,12 +96,12 @@ static SplitKernel split_of() {
 }
 typedef void (*TileFn)(const TileArgs);
 struct TileKernel {
-    TileFn fn;
+    TileFn fn, join;
     int smem, part_floats;
 };
 template <int NG>
 static TileKernel tile_of() {
-    return {k_attn_tile<NG>, TileShape<NG>::kSmem, kTileRows * (TileShape<NG>::kD + 2)};
+    return {k_attn_tile<NG>, k_attn_join<NG>, TileShape<NG>::kSmem, kTileRows * (TileShape<NG>::kD + 2)};
 }
 static TileKernel tile_kernel(int ng) {
     static const TileKernel table[4] = {tile_of<1>(), tile_of<2>(), tile_of<3>(), tile_of<4>()};
@@ -204,6 +205,7 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     const size_t o_part = take(part * sizeof(float));
     const size_t o_count = take(ctas * sizeof(int));
     kv->counts = ctas;
+    const size_t o_cut = take((size_t)kv->n_sms * sizeof(TileCut));
     const WtKernel wt = weights_kernel(cfg->head_dim / 64);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(wt.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, wt.smem);
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
@@ -218,6 +220,7 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     kv->lse = reinterpret_cast<float*>(kv->ws + o_lse);
     kv->part = reinterpret_cast<float*>(kv->ws + o_part);
     kv->count = reinterpret_cast<int*>(kv->ws + o_count);
+    kv->cut = reinterpret_cast<TileCut*>(kv->ws + o_cut);
     *out = kv;
     return MOE_OK;
 }
@@ -363,9 +366,10 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     const int64_t most = (int64_t)a.c.max_q * (a.c.hq / a.c.hkv);
     const bool tile = most > kSplitMaxRows;
     if (tile) {
-        TileArgs y{a, kv->part, kv->count, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
+        TileArgs y{a, kv->part, kv->cut, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
         const TileKernel k = tile_kernel(a.c.ng);
         KV_CK(kv_launch(1, k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
+        KV_CK(kv_launch(1, k.join, dim3(kv->n_sms, kTileRows / 32), kJoinThreads, 0, stream, y));
     }
     if (!tile || a.c.n_seqs > 1) {
         const int rt = most <= 8 ? 1 : 2;

@@ -26,8 +26,11 @@
 //                 codes turned in registers); scales and biases to fp32;
 //   warp 20       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
 //                 tile t, so it runs under the softmax of tile t.
-// Work is cut and joined as in the split kernel: equal runs of pages per CTA,
-// partial sums in the workspace, the last CTA to arrive joins an item.
+// Work is cut as in the split kernel: equal runs of pages per CTA.  An item that
+// CTA borders cut leaves partial sums in the workspace ([column / 4][row] of four
+// floats, so that a warp's 32 rows are one contiguous store); the CTA in which it
+// begins describes it, and k_attn_join, launched behind, joins the parts over all
+// SMs (one CTA per item would read its 9 parts of 128 KB in 40 us).
 #pragma once
 #include "kv_attn.cuh"
 #include "tcgen05.cuh"
@@ -66,10 +69,16 @@ struct TileShape {
     static_assert(kS + 2 * kStage <= 512, "tensor memory");
 };
 
+// An item cut by CTA borders: its parts lie in this CTA and the next parts - 1.
+struct TileCut {
+    int parts;                 // 0: none
+    int first, rows, rt, h;    // first row of the sequence, its (row, head) pairs, row tile, kv head
+};
+
 struct TileArgs {
     AttnArgs a;
-    float* part;               // [2 gridDim.x][128][D + 2]
-    int* count;                // [gridDim.x], zero between calls
+    float* part;               // [2 gridDim.x][128 (D + 2)]: sums, then maximum and total per row
+    TileCut* cut;              // [gridDim.x]: the cut item that begins in each CTA
     int min_rows_seq;          // sequences with fewer (row, head) pairs per kv head are not served here
 };
 
@@ -107,14 +116,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     using Sh = TileShape<NG>;
     constexpr int D = Sh::kD, KT = Sh::KT, HK = Sh::kHK;
     extern __shared__ uint8_t tl_raw[];
-    __shared__ __align__(8) uint64_t b_full[kTileSlots], b_s[2], b_p[2], b_pv[2];
+    __shared__ __align__(8) uint64_t b_q, b_full[kTileSlots], b_s[2], b_p[2], b_pv[2];
     __shared__ uint32_t s_tmem;
     __shared__ float s_mx[2][4][kTileRows], s_qs[NG][kTileRows];
     __shared__ float s_vmax[kTileSlots][4];
     __shared__ int s_ok[kTileSlots];
     __shared__ long long s_base0, s_total, s_per;
     __shared__ TileSeq s_q;
-    __shared__ int s_seq, s_last;
+    __shared__ int s_seq;
     const AttnArgs& a = x.a;
     const KvArgs& c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -172,9 +181,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     const long long total = s_total, per = s_per;
     long long u = blockIdx.x * per, base = s_base0;
     const long long u_end = min(total, u + per);
-    if (u >= u_end) return;
+    if (u >= u_end) {
+        if (tid == 0) x.cut[blockIdx.x].parts = 0;
+        return;
+    }
     int s = s_seq;
     TileSeq q = s_q;
+    bool cut = false;                                   // an item begins here and goes on in the next CTA
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
@@ -182,6 +195,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
+        mbar_init(&b_q, kTileSoft);
         for (int i = 0; i < kTileSlots; i++) mbar_init(&b_full[i], 4);      // converter warps
         for (int i = 0; i < 2; i++) {
             mbar_init(&b_s[i], 1);                                          // commits
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     bool ok = true;
-    uint32_t gt = 0;                                    // tiles of earlier segments: phases run on
+    uint32_t gt = 0, seg = 0;                           // tiles of earlier segments, and those: phases run on
     int rt = 0;                                         // row tile of the sequence, and the units before it
     long long rt_base = base;
 
@@ -228,36 +242,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
         const int first_low = a.window > 0 ? first_pos - a.window + 1 : 0;
         const int last_low = a.window > 0 ? last_pos - a.window + 1 : 0;
 
-        // Q: rows of 64 columns per group, columns in the order of the code pairs; the sign of
-        // the softmax scale goes with it
-        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-        for (int i = tid; i < NG * kTileRows * 8; i += kTileThreads) {
-            const int ch = i & 7, r = (i >> 3) & (kTileRows - 1), g = i >> 10;
-            const int rr = rt * kTileRows + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (rr < q.rows && a.scale != 0.f)
-                v = *reinterpret_cast<const uint4*>(a.q + (size_t)(q.first + rr / G) * a.q_stride +
-                                                    (size_t)(h * G + rr % G) * D + g * 64 + ch * 8);
-            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-            uint4 o;
-            o.x = __byte_perm(v.x, v.z, 0x5410);
-            o.y = __byte_perm(v.x, v.z, 0x7632);
-            o.z = __byte_perm(v.y, v.w, 0x5410);
-            o.w = __byte_perm(v.y, v.w, 0x7632);
-            *reinterpret_cast<uint4*>(gQ + g * (kTileRows * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) = o;
-            const float2 f0 = h2f(v.x), f1 = h2f(v.y), f2 = h2f(v.z), f3 = h2f(v.w);
-            float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-            if (ch == 0) s_qs[g][r] = sum;
-        }
-        fence_proxy_async_shared();
-        __syncthreads();
-
         if (warp < kTileSoft) {
             // ------------------------------------------------------ softmax --
             const int q4 = warp & 3, part = warp >> 2, r = 32 * q4 + lane;
+            // Q: rows of 64 columns per group, columns in the order of the code pairs; the sign
+            // of the softmax scale goes with it
+            {
+                const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+                constexpr int N = 2 * NG;               // 16-byte chunks per thread, all in flight
+                uint4 v[N];
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    const int i = tid + k * (kTileSoft * 32), ch = i & 7, rr = rt * kTileRows + ((i >> 3) & (kTileRows - 1));
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (rr < q.rows && a.scale != 0.f)
+                        v[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(q.first + rr / G) * a.q_stride +
+                                                               (size_t)(h * G + rr % G) * D + (i >> 10) * 64 + ch * 8);
+                }
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    const int i = tid + k * (kTileSoft * 32), ch = i & 7, r = (i >> 3) & (kTileRows - 1), g = i >> 10;
+                    v[k].x ^= flip; v[k].y ^= flip; v[k].z ^= flip; v[k].w ^= flip;
+                    *reinterpret_cast<uint4*>(gQ + g * (kTileRows * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) =
+                        make_uint4(__byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
+                                   __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
+                    const float2 f0 = h2f(v[k].x), f1 = h2f(v[k].y), f2 = h2f(v[k].z), f3 = h2f(v[k].w);
+                    float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    if (ch == 0) s_qs[g][r] = sum;
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_q);
+                named_bar(5, kTileSoft * 32);           // the rows' sums
+            }
             const uint32_t t_row = tmem + ((uint32_t)(32 * q4) << 16);
             const int rr = min(rt * kTileRows + r, q.rows - 1);
             const int pos = p0 + rr / G, low = a.window > 0 ? pos - a.window + 1 : 0;
@@ -425,7 +445,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            *reinterpret_cast<float4*>(slot + (size_t)r * D + col + 4 * e) =
+                            *reinterpret_cast<float4*>(slot + ((size_t)(col / 4 + e) * kTileRows + r) * 4) =
                                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
@@ -445,83 +465,90 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             const int32_t* trow = c.table + (size_t)s * c.max_pages;
             const int vw = ct & 7, vk = (ct >> 3) % (KT / 8), vg = (ct >> 3) / (KT / 8);   // V: 8 x 8 codes each
             const int eg = ct / KT, ee = ct % KT;                                          // scale and bias of one entry
-            uint4 kw[2];
-            uint32_t vv[8], ks = 0, vs = 0;
-            bool page = false;
-            const auto load = [&](int t) {
+            // a tile's raw bytes, two sets in turn: the next tile's loads are in flight while
+            // one is converted
+            struct Raw {
+                uint4 k[2];
+                uint32_t v[8], ks, vs;
+                bool page;
+            } raw[2];
+            const auto page_at = [&](int t) {            // -1: behind the last entry
                 const int pg = pg0 + t / Sh::kSub;
-                const int id = pg * kKvPage < q.len ? trow[pg] : -1;
-                page = (unsigned)id < (unsigned)c.n_pages;
-                if (!page) {
-                    if (ct == 0 && pg * kKvPage < q.len) kv_flag(c.status);
-                    kw[0] = kw[1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) vv[i] = 0;
-                    ks = vs = 0;
-                    return;
-                }
-                const uint8_t* tile = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG);
-                const int sub = (t % Sh::kSub) * KT;
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int n = i * 128 + ct, g = n / (KT * 2);
-                    if (g < NG)
-                        kw[i] = __ldg(reinterpret_cast<const uint4*>(tile + g * 2048 + sub * 32 + (n % (KT * 2)) * 16));
-                }
-                if (vg < NG) {
-                    const uint8_t* v = tile + 2304 * NG + vg * 2048 + (sub + vk * 8) * 32 + vw * 4;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) vv[i] = __ldg(reinterpret_cast<const uint32_t*>(v + i * 32));
-                }
-                if (eg < NG) {
-                    const uint8_t* sp = tile + 2048 * NG + (eg * kKvPage + sub + ee) * 4;
-                    ks = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                    vs = __ldg(reinterpret_cast<const uint32_t*>(sp + 2304 * NG));
-                }
+                return t < T && pg * kKvPage < q.len ? trow[pg] : -1;
             };
-            load(0);
-            for (int t = 0; ok && t < T; t++) {
+            int id = page_at(0);                         // of the next tile to load, read one ahead
+            const auto load = [&](Raw& w, int t) {
+                w.page = (unsigned)id < (unsigned)c.n_pages;
+                if (!w.page) {
+                    if (ct == 0 && (pg0 + t / Sh::kSub) * kKvPage < q.len) kv_flag(c.status);
+                    w.k[0] = w.k[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) w.v[i] = 0;
+                    w.ks = w.vs = 0;
+                } else {
+                    const uint8_t* tile = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG);
+                    const int sub = (t % Sh::kSub) * KT;
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int n = i * 128 + ct, g = n / (KT * 2);
+                        if (g < NG)
+                            w.k[i] = __ldg(reinterpret_cast<const uint4*>(tile + g * 2048 + sub * 32 + (n % (KT * 2)) * 16));
+                    }
+                    if (vg < NG) {
+                        const uint8_t* v = tile + 2304 * NG + vg * 2048 + (sub + vk * 8) * 32 + vw * 4;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) w.v[i] = __ldg(reinterpret_cast<const uint32_t*>(v + i * 32));
+                    }
+                    if (eg < NG) {
+                        const uint8_t* sp = tile + 2048 * NG + (eg * kKvPage + sub + ee) * 4;
+                        w.ks = __ldg(reinterpret_cast<const uint32_t*>(sp));
+                        w.vs = __ldg(reinterpret_cast<const uint32_t*>(sp + 2304 * NG));
+                    }
+                }
+                id = page_at(t + 1);
+            };
+            const auto convert = [&](const Raw& w, int t) {
                 const uint32_t n = gt + t;
                 const int slot = n % kTileSlots;
                 // the slot's last user, P V of tile t - 3, has ended (tiles of earlier segments: all have)
                 if (t >= kTileSlots)
                     ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(n - kTileSlots) & 1],
                                                                 ((n - kTileSlots) >> 1) & 1u, c.stop));
-                if (!ok) break;
+                if (!ok) return;
                 uint8_t* gk = gSlots + slot * Sh::kSlot;
                 uint8_t* gv = gk + Sh::kK;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     const int nn = i * 128 + ct, g = nn / (KT * 2), r = (nn >> 1) % KT, hf = nn & 1;
                     if (g < NG) {
-                        const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+                        const uint32_t word[4] = {w.k[i].x, w.k[i].y, w.k[i].z, w.k[i].w};
 #pragma unroll
                         for (int k = 0; k < 4; k++)
                             *reinterpret_cast<uint4*>(gk + g * (KT * 128) + r * 128 + (((hf * 4 + k) ^ (r & 7)) << 4)) =
-                                codes_centred(w[k]);
+                                codes_centred(word[k]);
                     }
                 }
                 if (vg < NG) {
-                    uint4 lo[4], hi[4];                  // entries 2i, 2i + 1: columns 0..3 and 4..7
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        lo[i] = codes_centred(__byte_perm(vv[2 * i], vv[2 * i + 1], 0x5410));
-                        hi[i] = codes_centred(__byte_perm(vv[2 * i], vv[2 * i + 1], 0x7632));
-                    }
+                    for (int hf = 0; hf < 2; hf++) {     // columns 0..3, then 4..7 of the block
+                        uint4 e[4];                      // entries 2i, 2i + 1
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const uint4(&x4)[4] = j < 4 ? lo : hi;
-                        const auto get = [&](int i) { return (j & 3) == 0 ? x4[i].x : (j & 3) == 1 ? x4[i].y : (j & 3) == 2 ? x4[i].z : x4[i].w; };
-                        *reinterpret_cast<uint4*>(gv + vg * (64 * 128) + (8 * vw + j) * 128 + ((vk ^ j) << 4)) =
-                            make_uint4(get(0), get(1), get(2), get(3));
+                        for (int i = 0; i < 4; i++)
+                            e[i] = codes_centred(__byte_perm(w.v[2 * i], w.v[2 * i + 1], hf ? 0x7632 : 0x5410));
+                        uint8_t* dst = gv + vg * (64 * 128) + (8 * vw + 4 * hf) * 128;
+                        const int z = 4 * hf;
+                        *reinterpret_cast<uint4*>(dst + ((vk ^ z) << 4)) = make_uint4(e[0].x, e[1].x, e[2].x, e[3].x);
+                        *reinterpret_cast<uint4*>(dst + 128 + ((vk ^ (z + 1)) << 4)) = make_uint4(e[0].y, e[1].y, e[2].y, e[3].y);
+                        *reinterpret_cast<uint4*>(dst + 256 + ((vk ^ (z + 2)) << 4)) = make_uint4(e[0].z, e[1].z, e[2].z, e[3].z);
+                        *reinterpret_cast<uint4*>(dst + 384 + ((vk ^ (z + 3)) << 4)) = make_uint4(e[0].w, e[1].w, e[2].w, e[3].w);
                     }
                 }
                 // scales: entries that no row of the tile sees count as zero, whatever they hold
                 float vm = 0.f;
                 if (eg < NG) {
                     const int j = (pg0 + t / Sh::kSub) * kKvPage + (t % Sh::kSub) * KT + ee;
-                    const bool in = page && j <= last_pos && j >= first_low;
-                    const float2 fk = in ? h2f(ks) : make_float2(0.f, 0.f), fv = in ? h2f(vs) : make_float2(0.f, 0.f);
+                    const bool in = w.page && j <= last_pos && j >= first_low;
+                    const float2 fk = in ? h2f(w.ks) : make_float2(0.f, 0.f), fv = in ? h2f(w.vs) : make_float2(0.f, 0.f);
                     float2* sc = gScale + (size_t)slot * 2 * NG * KT + eg * KT + ee;
                     sc[0] = make_float2(fk.x, fmaf(8.f, fk.x, fk.y));
                     sc[NG * KT] = make_float2(fv.x, fmaf(8.f, fv.x, fv.y));
@@ -530,11 +557,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
                 if (lane == 0) s_vmax[slot][cw] = vm;
-                if (ct == 0) s_ok[slot] = page;
-                if (t + 1 < T) load(t + 1);
+                if (ct == 0) s_ok[slot] = w.page;
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_full[slot]);
+            };
+            load(raw[0], 0);
+            for (int t = 0; ok && t < T; t += 2) {
+                if (t + 1 < T) load(raw[1], t + 1);
+                convert(raw[0], t);
+                if (t + 2 < T) load(raw[0], t + 2);
+                if (ok && t + 1 < T) convert(raw[1], t + 1);
             }
         } else if (lane == 0) {
             // --------------------------------------------------- MMA issuer --
@@ -556,6 +589,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 mma_commit(&b_pv[st]);
                 return true;
             };
+            if (!fused_wait_bar(&b_q, seg & 1u, c.stop)) ok = false;
             int done = 0, asked = 0;                     // tiles whose P V and whose Q K have been issued
             for (int t = 0; ok && t < T; t++) {
                 const uint32_t n = gt + t;
@@ -588,57 +622,77 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             if (!ok && asked > 0) mma_drain_wait(&b_s[(gt + asked - 1) & 1], ((gt + asked - 1) >> 1) & 1u);
         }
         gt += T;
-        // a role that gave up has recorded it: all leave together
+        seg++;
+        if (ib >= blockIdx.x * per && u < ie) {         // the item goes on in the next CTA
+            cut = true;
+            if (tid == 0) x.cut[blockIdx.x] = TileCut{(int)((ie - 1) / per) - (int)blockIdx.x + 1, q.first, q.rows, rt, h};
+        }
+        // a role that gave up has recorded it: all leave together; shared memory is free then
         if (__syncthreads_or(!ok)) {
-            ok = false;
+            cut = false;
             break;
         }
-        const bool whole = u == ie && ib >= blockIdx.x * per;
-        if (!whole) {
-            const int c0 = (int)(ib / per), c1 = (int)((ie - 1) / per);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(x.count + c0, 1) == c1 - c0;
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const auto at = [&](int b) { return x.part + (size_t)(2 * b + (b == c0 ? 1 : 0)) * (kTileRows * (D + 2)); };
-                for (int i = tid; i < kTileRows * (D / 4); i += kTileThreads) {
-                    const int r = i / (D / 4), d = (i % (D / 4)) * 4, rr = rt * kTileRows + r;
-                    if (rr >= q.rows) continue;
-                    float M = -INFINITY, L = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int b = c0; b <= c1; b++) M = fmaxf(M, __ldcg(at(b) + kTileRows * D + r));
-                    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 8
-                    for (int b = c0; b <= c1; b++) {
-                        const float mb = __ldcg(at(b) + kTileRows * D + r), lb = __ldcg(at(b) + kTileRows * D + kTileRows + r);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(at(b) + (size_t)r * D + d));
-                        const float f = mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref);
-                        L = fmaf(f, lb, L);
-                        o.x = fmaf(f, v.x, o.x);
-                        o.y = fmaf(f, v.y, o.y);
-                        o.z = fmaf(f, v.z, o.z);
-                        o.w = fmaf(f, v.w, o.w);
-                    }
-                    const float f = L == 0.f ? 0.f : 1.f / L;
-                    const int head = h * G + rr % G;
-                    *reinterpret_cast<uint2*>(a.out + (size_t)(q.first + rr / G) * a.out_stride + (size_t)head * D + d) =
-                        make_uint2(f2h(o.x * f, o.y * f), f2h(o.z * f, o.w * f));
-                    if (d == 0) a.lse[(size_t)(q.first + rr / G) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-                }
-                if (tid == 0) x.count[c0] = 0;
-            }
-        }
-        __syncthreads();                                // shared memory is free for the next segment
     }
+    if (tid == 0 && !cut) x.cut[blockIdx.x].parts = 0;
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x: rows 32 blockIdx.y ..
+// of its tile, one per lane, 16 columns a warp at a time.
+constexpr int kJoinThreads = 256;
+
+template <int NG>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const TileArgs x) {
+    constexpr int D = 64 * NG;
+    constexpr size_t kSlot = (size_t)kTileRows * (D + 2);
+    kv_begin();
+    const TileCut c = x.cut[blockIdx.x];
+    const int r = blockIdx.y * 32 + (threadIdx.x & 31), rr = c.rt * kTileRows + r;
+    if (c.parts <= 0 || rr >= c.rows) return;
+    const int G = x.a.c.hq / x.a.c.hkv, head = c.h * G + rr % G;
+    // the first part is its CTA's second slot, the others their CTAs' first
+    const auto at = [&](int b) { return x.part + (size_t)(2 * ((int)blockIdx.x + b) + (b == 0 ? 1 : 0)) * kSlot; };
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < c.parts; b++) M = fmaxf(M, at(b)[kTileRows * D + r]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 8
+    for (int b = 0; b < c.parts; b++) {
+        const float mb = at(b)[kTileRows * D + r], lb = at(b)[kTileRows * D + kTileRows + r];
+        L = fmaf(mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref), lb, L);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t row = (size_t)c.first + rr / G;
+    for (int col = (threadIdx.x >> 5) * 16; col < D; col += kJoinThreads / 32 * 16) {
+        float o[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = 0.f;
+#pragma unroll 4
+        for (int b = 0; b < c.parts; b++) {
+            const float mb = at(b)[kTileRows * D + r], lb = at(b)[kTileRows * D + kTileRows + r];
+            const float f = mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float4 v = *reinterpret_cast<const float4*>(at(b) + ((size_t)(col / 4 + e) * kTileRows + r) * 4);
+                o[4 * e] = fmaf(f, v.x, o[4 * e]);
+                o[4 * e + 1] = fmaf(f, v.y, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(f, v.z, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(f, v.w, o[4 * e + 3]);
+            }
+        }
+        __half* out = x.a.out + row * x.a.out_stride + (size_t)head * D + col;
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            *reinterpret_cast<uint4*>(out + 8 * e) =
+                make_uint4(f2h(o[8 * e] * inv, o[8 * e + 1] * inv), f2h(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                           f2h(o[8 * e + 4] * inv, o[8 * e + 5] * inv), f2h(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+    }
+    if (threadIdx.x < 32) x.a.lse[row * x.a.c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace moeq4
