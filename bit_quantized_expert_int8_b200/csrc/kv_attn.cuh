@@ -61,6 +61,30 @@ __device__ __forceinline__ uint32_t f2h(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// floor(log2 x) of a positive normal x, and 2^e for -126 <= e <= 127.
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // The same pairs as fp16 c - 8.
 __device__ __forceinline__ uint4 codes_centred(uint32_t w) {
     const uint32_t u = w >> 8;
@@ -74,6 +98,19 @@ __device__ __forceinline__ uint4 codes_centred(uint32_t w) {
         r[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// And as fp16 c.
+__device__ __forceinline__ void codes_exact(uint32_t w, uint32_t (&o)[4]) {
+    const uint32_t u = w >> 8;
+    const uint32_t v[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
+                           (u & 0x000F000Fu) | 0x64006400u, (u & 0x00F000F0u) | 0x54005400u};
+    const __half2 o0 = __float2half2_rn(-1024.f), o1 = __float2half2_rn(-64.f);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&v[k]), k & 1 ? o1 : o0);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

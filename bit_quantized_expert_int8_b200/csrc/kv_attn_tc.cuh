@@ -2,30 +2,37 @@
 // (prompt chunks) on the 5th-generation tensor cores.
 //
 // Rows of one kv head are its (row, query head) pairs; an item is (sequence,
-// tile of 128 rows, kv head).  Per tile of KT entries and group g of 64 columns
-//   acc_g[r][j] = q_g[r] . (c_g[j] - 8)            tcgen05, Q and codes in shared memory
-//   S = sum_g s_jg acc_g + (b_jg + 8 s_jg) sum(q_g[r])                    CUDA cores
-//   p = exp(S - max),  P_g = fp16(p s_jg)          into tensor memory, over acc
-//   O_g[r][d] += P_g[r] . (c_g[.][d] - 8)          tcgen05, P from tensor memory
-//   B_g[r] += p (b_jg + 8 s_jg)                                           CUDA cores
-// and out = (O_g + B_g) / sum p.  The codes are exact operands, so the scores are
-// as exact as fp32 sums are; the one rounding is that of p s to fp16 (relative
-// 2^-12 per entry, averaged over the entries seen: below the rounding of the
-// output itself).  Codes are centred (c - 8) so that this rounding is weighed
-// with values around zero.  P is kept in range by a power of two per CTA (unit)
-// from the largest scale of V in a tile; the row maximum moves only when it grows
-// by more than 2^8, and only then is O rescaled.
+// tile of 128 rows, kv head).  Per page of 64 entries
+//   S[r][j] = q[r] . k[j]       tcgen05, Q and K in shared memory
+//   p = exp(S - max)            one row per pair of threads, fp16 P over S in tensor memory
+//   O[r][d] += P[r] . v[.][d]   tcgen05, P from tensor memory, V in shared memory
+// K enters as two fp16 operands, hi = fp16(s c + b) and lo = fp16(s c + b - hi),
+// so the scores are as exact as fp32 sums are.  (With the raw codes as operands
+// and the groups' scales folded in by the softmax threads, as the few-row kernel
+// does it, every thread reads every entry's scales from shared memory: 512
+// 16-byte broadcasts a tile, 5,000 cycles; this way a tile costs 1,500.)  V and p
+// are rounded to fp16 once, a relative 2^-12 each on average, below the rounding
+// of the output.  K and V are scaled by powers of two, so that no value leaves
+// fp16's range: K's (per page) divides the softmax scale, V's (held until a page
+// exceeds it) leaves at the end.  The row maximum moves only when it grows by more
+// than 2^8, and only then is O rescaled.  Groups of V that are not finite enter as
+// zeros; rows that see one get a NaN in its columns at the end, so that masked
+// rows (p = 0) stay clean.
 //
-// Roles, meeting at mbarriers (every wait bounded):
-//   warps 0..15   scores and softmax: warp w holds rows 32 (w % 4) .. of the tile
-//                 (TMEM lanes) and quarter w / 4 of its entries; the four quarters
-//                 of a row exchange their maximum through shared memory;
-//   warps 16..19  converters: codes from global memory (the next tile's loads in
+// Roles, meeting at mbarriers (every wait bounded; each barrier that frees a ring
+// slot belongs to that slot, so no waiter can fall two phases behind):
+//   warps 0..7    softmax: warp w holds rows 32 (w % 4) .. of the tile (TMEM lanes)
+//                 and half w / 4 of its entries; the halves of a row exchange
+//                 their maximum through shared memory.  They bring Q to tensor memory.
+//   warps 8..15   converters: codes from global memory (the next page's loads in
 //                 flight while one is converted) to fp16 operands in shared memory,
-//                 128-byte swizzle: K entry-major, V transposed (8 x 8 blocks of
-//                 codes turned in registers); scales and biases to fp32;
-//   warp 20       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
-//                 tile t, so it runs under the softmax of tile t.
+//                 128-byte swizzle: K entry-major, V transposed (8 x 4 blocks of
+//                 codes turned in registers);
+//   warp 16       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
+//                 tile t, so it runs under the softmax of tile t;
+//   warp 17       walker (one thread): what the CTA does next, a segment ahead;
+//   warps 18, 19  scales and biases of K and of V, pages ahead of the converters:
+//                 the powers of two, which entries count, what is not finite.
 // Work is cut as in the split kernel: equal runs of pages per CTA.  An item that
 // CTA borders cut leaves partial sums in the workspace ([column / 4][row] of four
 // floats, so that a warp's 32 rows are one contiguous store); the CTA in which it
@@ -39,34 +46,40 @@
 namespace moeq4 {
 
 constexpr int kTileRows = 128;
-constexpr int kTileSoft = 16;          // softmax warps: 4 per 32 rows
-constexpr int kTileWarps = kTileSoft + 5;
+constexpr int kTileSoft = 8;           // softmax warps: 2 per 32 rows
+constexpr int kTileConv = 8;           // converter warps
+constexpr int kTileWarps = kTileSoft + kTileConv + 4;    // the issuer's warpgroup: one warp works
+// Registers: 96 a thread at launch (640 threads); the issuer's warpgroup gives some of
+// its own up to the converters: 256 x 96 + 256 x 120 + 128 x 48 <= 640 x 96.
+constexpr int kTileConvRegs = 120, kTileIssueRegs = 48;
+static_assert((kTileSoft * 96 + kTileConv * kTileConvRegs + 4 * kTileIssueRegs) <= kTileWarps * 96, "registers");
 constexpr int kTileThreads = kTileWarps * 32;
-constexpr int kTileSlots = 3;
 constexpr int kTileItemCost = 4;       // pages an item costs beside its own
 constexpr int kTileMinUnits = 6;       // pages per CTA at least
-
-template <bool B>
-struct BoolC {
-    static constexpr bool value = B;
-};
+constexpr int kTileMeta = 16;          // pages whose facts are kept for the softmax
+constexpr int kTileScales = 4;         // pages whose scales are kept for the converters
+constexpr float kTileLift = 6.f;       // p is taken times 2^6: at most 2^14 with a maximum 2^8 behind
 
 template <int NG>
 struct TileShape {
     static constexpr int kD = 64 * NG;
-    static constexpr int KT = NG <= 2 ? 64 : 32;                // entries per tile
-    static constexpr int kSub = kKvPage / KT;                   // tiles per page
-    static constexpr int kHK = KT / 4;                          // entries per softmax thread
-    static constexpr int kQ = NG * kTileRows * 128;             // bytes
-    static constexpr int kK = NG * KT * 128;
-    static constexpr int kV = NG * 64 * 128;                    // 64 columns x KT entries, rows of 128 bytes
-    static constexpr int kScale = NG * KT * 8;                  // (scale, bias + 8 scale) of K or V
-    static constexpr int kSlot = kK + kV;
-    static constexpr int kSmem = kQ + kTileSlots * (kSlot + 2 * kScale) + 1024;
-    static constexpr uint32_t kO = 0;                           // TMEM columns: O, then two score stages
-    static constexpr uint32_t kS = NG * 64;
-    static constexpr uint32_t kStage = NG * KT;
-    static_assert(kS + 2 * kStage <= 512, "tensor memory");
+    static constexpr int kK = 2 * NG * kKvPage * 128;           // bytes: hi, then lo
+    static constexpr int kV = NG * 64 * 128;                    // columns x entries
+    static constexpr int kKRing = 2, kVRing = 2;
+    static constexpr int kSmem = kKRing * kK + kVRing * kV + 1024;
+    static constexpr uint32_t kO = 0;                           // TMEM columns: O, two score stages, Q
+    static constexpr uint32_t kS = kD;
+    static constexpr uint32_t kQ = kS + 2 * kKvPage;
+    static_assert(kQ + kD / 2 <= 512, "tensor memory");
+};
+
+// What the scale warps tell the softmax warps of a page.
+struct TileMeta {
+    float kinv;                // 1 / K's power of two
+    float vexp;                // log2 of V's
+    int ok;                    // the page index is usable
+    uint32_t bad[4][2];        // per group: entries whose V is not finite
+    int any;                   // some are
 };
 
 // An item cut by CTA borders: its parts lie in this CTA and the next parts - 1.
@@ -111,84 +124,140 @@ __device__ __forceinline__ TileSeq tile_seq(const TileArgs& x, int s, bool repor
     return q;
 }
 
+// One CTA's run of pages of one item.
+struct TileSegment {
+    int T;                     // pages; 0: no more work
+    int s, first, len, rows;   // sequence, its first row, entries, (row, head) pairs
+    int p0;                    // entry of its row 0
+    int rt, h, pg0;            // row tile, kv head, first page
+    int whole;                 // the item lies in this segment
+    int slot;                  // of its partial sums: 1 when it begins here and goes on
+};
+
+// Finds a CTA's segments in order.
+struct TileWalk {
+    long long u, u_end, per, base, rt_base;   // next unit, end of the run; units before the sequence and the row tile
+    int s, rt;
+    TileSeq q;
+
+    // A warp: units of all sequences, this CTA's run, the sequence it begins in.
+    __device__ __forceinline__ void start(const TileArgs& x, int lane) {
+        const int n_seqs = x.a.c.n_seqs;
+        long long total = 0;
+        q.units = 0;
+        for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+            q.units = 0;
+            if (s0 + lane < n_seqs) q = tile_seq(x, s0 + lane, blockIdx.x == 0);
+            total += q.units;
+        }
+        total = warp_sum(total);
+        const long long n = total + gridDim.x - 1;
+        per = max(n >> 32 ? n / gridDim.x : (long long)((unsigned)n / gridDim.x), (long long)kTileMinUnits);
+        u = blockIdx.x * per;
+        u_end = min(total, u + per);
+        base = rt_base = 0;
+        s = rt = 0;
+        if (lane == 0) x.cut[blockIdx.x].parts = 0;              // until a cut item begins here
+        if (u >= u_end) return;
+        int at = 0;
+        for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+            if (n_seqs > 32) {                                   // else q holds it already
+                q.units = 0;
+                if (s0 + lane < n_seqs) q = tile_seq(x, s0 + lane, false);
+            }
+            long long inc = q.units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
+            if (hit) {
+                at = __ffs(hit) - 1;
+                s = s0 + at;
+                base += __shfl_sync(0xffffffffu, inc - q.units, at);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        rt_base = base;
+        if (lane == 0) q = tile_seq(x, s, false);
+    }
+
+    // One thread: the next segment.
+    __device__ __forceinline__ TileSegment next(const TileArgs& x) {
+        const KvArgs& c = x.a.c;
+        TileSegment g{};
+        if (u < u_end) {
+            int plo, np;
+            while (true) {                                       // row tile that holds unit u
+                while (rt >= q.tiles) {
+                    base += q.units;
+                    q = tile_seq(x, ++s, false);
+                    rt = 0;
+                    rt_base = base;
+                }
+                tile_pages(x, q, rt, &plo, &np);
+                const long long w = (long long)(np + kTileItemCost) * c.hkv;
+                if (u < rt_base + w) break;
+                rt_base += w;
+                rt++;
+            }
+            const int h = (int)(u - rt_base) / (np + kTileItemCost);
+            // the item's pages stand at units ib .. ie - 1, behind its fixed cost
+            const long long ib = rt_base + (long long)h * (np + kTileItemCost) + kTileItemCost, ie = ib + np;
+            u = max(u, ib);
+            if (u < u_end) {
+                g.T = (int)(min(u_end, ie) - u);
+                g.s = s;
+                g.first = q.first;
+                g.len = q.len;
+                g.rows = q.rows;
+                g.p0 = q.len - q.n;
+                g.rt = rt;
+                g.h = h;
+                g.pg0 = plo + (int)(u - ib);
+                u = min(u_end, ie);
+                const bool begins = ib >= blockIdx.x * per;
+                g.whole = begins && u == ie;
+                g.slot = begins;
+                if (begins && u < ie)
+                    x.cut[blockIdx.x] = TileCut{(int)((ie - 1) / per) - (int)blockIdx.x + 1, q.first, q.rows, rt, h};
+                return g;
+            }
+        }
+        return g;
+    }
+};
+
 template <int NG>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x) {
     using Sh = TileShape<NG>;
-    constexpr int D = Sh::kD, KT = Sh::KT, HK = Sh::kHK;
+    constexpr int D = Sh::kD, KT = kKvPage, HK = KT / 2, KR = Sh::kKRing, VR = Sh::kVRing;
     extern __shared__ uint8_t tl_raw[];
-    __shared__ __align__(8) uint64_t b_q, b_full[kTileSlots], b_s[2], b_p[2], b_pv[2];
+    __shared__ __align__(8) uint64_t b_q, b_k[KR], b_kf[KR], b_v[VR], b_pv[VR], b_s[2], b_p[2];
+    __shared__ __align__(8) uint64_t b_sc[kTileScales], b_scf[kTileScales];
     __shared__ uint32_t s_tmem;
-    __shared__ float s_mx[2][4][kTileRows], s_qs[NG][kTileRows];
-    __shared__ float s_vmax[kTileSlots][4];
-    __shared__ int s_ok[kTileSlots];
-    __shared__ long long s_base0, s_total, s_per;
-    __shared__ TileSeq s_q;
-    __shared__ int s_seq;
+    __shared__ float s_mx[2][2][kTileRows], s_sum[2][NG + 1][kTileRows];
+    // scaled by the page's powers of two: scale then bias of every entry
+    __shared__ __align__(16) __half s_sc[kTileScales][2][2][NG][KT];
+    __shared__ TileMeta s_meta[kTileMeta];
+    __shared__ TileSegment s_seg[2];
     const AttnArgs& a = x.a;
     const KvArgs& c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = c.hq / c.hkv;
     const uint32_t sbase = (smem_u32(tl_raw) + 1023u) & ~1023u;
-    uint8_t* gbase = tl_raw + (sbase - smem_u32(tl_raw));
-    const uint32_t sQ = sbase, sSlots = sbase + Sh::kQ;
-    uint8_t* gQ = gbase;
-    float(*s_sum)[NG + 1][kTileRows] = reinterpret_cast<float(*)[NG + 1][kTileRows]>(gQ);   // once Q has been used
-    uint8_t* gSlots = gbase + Sh::kQ;
-    float2* gScale = reinterpret_cast<float2*>(gSlots + kTileSlots * Sh::kSlot);   // [slot][K, V][g][entry]
+    uint8_t* gK = tl_raw + (sbase - smem_u32(tl_raw));
+    uint8_t* gV = gK + KR * Sh::kK;
+    const uint32_t sK = sbase, sV = sK + KR * Sh::kK;
 
     kv_begin();
-    if (warp == 0) {
-        long long total = 0;
-        TileSeq q{};
-        for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-            q.units = 0;
-            if (s0 + lane < c.n_seqs) q = tile_seq(x, s0 + lane, blockIdx.x == 0);
-            total += q.units;
-        }
-        total = warp_sum(total);
-        const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kTileMinUnits);
-        const long long u = blockIdx.x * per;
-        long long base = 0;
-        if (u < total)
-            for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
-                if (c.n_seqs > 32) {
-                    q.units = 0;
-                    if (s0 + lane < c.n_seqs) q = tile_seq(x, s0 + lane, false);
-                }
-                long long inc = q.units;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
-                if (hit) {
-                    if (lane == __ffs(hit) - 1) {
-                        s_q = q;
-                        s_seq = s0 + lane;
-                        s_base0 = base + inc - q.units;
-                    }
-                    break;
-                }
-                base += __shfl_sync(0xffffffffu, inc, 31);
-            }
-        if (lane == 0) {
-            s_total = total;
-            s_per = per;
-        }
+    TileWalk walk;
+    if (warp == kTileSoft + kTileConv + 1) {
+        walk.start(x, lane);
+        if (lane == 0) s_seg[0] = walk.next(x);
     }
-    __syncthreads();
-    const long long total = s_total, per = s_per;
-    long long u = blockIdx.x * per, base = s_base0;
-    const long long u_end = min(total, u + per);
-    if (u >= u_end) {
-        if (tid == 0) x.cut[blockIdx.x].parts = 0;
-        return;
-    }
-    int s = s_seq;
-    TileSeq q = s_q;
-    bool cut = false;                                   // an item begins here and goes on in the next CTA
-
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
                      : "memory");
@@ -196,11 +265,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     }
     if (tid == 0) {
         mbar_init(&b_q, kTileSoft);
-        for (int i = 0; i < kTileSlots; i++) mbar_init(&b_full[i], 4);      // converter warps
-        for (int i = 0; i < 2; i++) {
-            mbar_init(&b_s[i], 1);                                          // commits
-            mbar_init(&b_p[i], kTileSoft);                                  // softmax warps
+        for (int i = 0; i < KR; i++) {
+            mbar_init(&b_k[i], kTileConv);
+            mbar_init(&b_kf[i], 1);                                         // commits
+        }
+        for (int i = 0; i < VR; i++) {
+            mbar_init(&b_v[i], kTileConv);
             mbar_init(&b_pv[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&b_s[i], 2);              // the commit, and the issuer for what it saw of the page
+            mbar_init(&b_p[i], kTileSoft);
+        }
+        for (int i = 0; i < kTileScales; i++) {
+            mbar_init(&b_sc[i], 2);                                         // the two scale warps
+            mbar_init(&b_scf[i], kTileConv);
         }
         fence_mbar_init();
     }
@@ -209,161 +288,120 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     bool ok = true;
-    uint32_t gt = 0, seg = 0;                           // tiles of earlier segments, and those: phases run on
-    int rt = 0;                                         // row tile of the sequence, and the units before it
-    long long rt_base = base;
+    uint32_t gt = 0;                                    // tiles of earlier segments: phases run on
+    // end of a segment: a role that gave up has recorded it, and all leave together
+#define TILE_SEGMENTS(seg, g)                                                     \
+    for (int seg = 0;; seg++) {                                                   \
+        const TileSegment g = s_seg[seg & 1];                                     \
+        if (g.T == 0) break;
+#define TILE_SEGMENTS_END(g)                                                      \
+        gt += g.T;                                                                \
+        if (__syncthreads_or(!ok)) break;                                         \
+    }
 
-    while (u < u_end) {
-        int plo, np;
-        while (true) {                                  // row tile that holds unit u
-            while (rt >= q.tiles) {
-                base += q.units;
-                s++;
-                q = tile_seq(x, s, false);
-                rt = 0;
-                rt_base = base;
-            }
-            tile_pages(x, q, rt, &plo, &np);
-            const long long w = (long long)(np + kTileItemCost) * c.hkv;
-            if (u < rt_base + w) break;
-            rt_base += w;
-            rt++;
-        }
-        const int h = (int)((u - rt_base) / (np + kTileItemCost));
-        const long long ib = rt_base + (long long)h * (np + kTileItemCost) + kTileItemCost, ie = ib + np;
-        u = max(u, ib);
-        if (u >= u_end) break;
-        const int pg0 = plo + (int)(u - ib), pg1 = plo + (int)(min(u_end, ie) - ib);
-        u = min(u_end, ie);
-        const int p0 = q.len - q.n;
-        const int T = (pg1 - pg0) * Sh::kSub;           // tiles of this segment
-        const int first_pos = p0 + rt * kTileRows / G;  // least and greatest row
-        const int last_pos = p0 + (min((rt + 1) * kTileRows, q.rows) - 1) / G;
-        const int first_low = a.window > 0 ? first_pos - a.window + 1 : 0;
-        const int last_low = a.window > 0 ? last_pos - a.window + 1 : 0;
-
-        if (warp < kTileSoft) {
-            // ------------------------------------------------------ softmax --
-            const int q4 = warp & 3, part = warp >> 2, r = 32 * q4 + lane;
-            // Q: rows of 64 columns per group, columns in the order of the code pairs; the sign
-            // of the softmax scale goes with it
+    if (warp < kTileSoft) {
+        // ---------------------------------------------------------- softmax --
+        TILE_SEGMENTS(seg, sg)
+            const int T = sg.T, rt = sg.rt, h = sg.h, p0 = sg.p0, pg0 = sg.pg0;
+            const int first_pos = p0 + rt * kTileRows / G;      // least and greatest row
+            const int last_pos = p0 + (min((rt + 1) * kTileRows, sg.rows) - 1) / G;
+            const int last_low = a.window > 0 ? last_pos - a.window + 1 : 0;
+            const int q4 = warp & 3, half = warp >> 2, r = 32 * q4 + lane;
+            const uint32_t t_row = tmem + ((uint32_t)(32 * q4) << 16);
+            // Q to tensor memory: this half's columns of the row, in the order of the code pairs;
+            // the sign of the softmax scale goes with it
             {
                 const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-                constexpr int N = 2 * NG;               // 16-byte chunks per thread, all in flight
-                uint4 v[N];
+                const int qr = rt * kTileRows + r;
+                const bool on = qr < sg.rows && a.scale != 0.f;
+                const __half* qp = a.q + (size_t)(sg.first + min(qr, sg.rows - 1) / G) * a.q_stride +
+                                   (size_t)(h * G + min(qr, sg.rows - 1) % G) * D + half * (NG * 32);
 #pragma unroll
-                for (int k = 0; k < N; k++) {
-                    const int i = tid + k * (kTileSoft * 32), ch = i & 7, rr = rt * kTileRows + ((i >> 3) & (kTileRows - 1));
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (rr < q.rows && a.scale != 0.f)
-                        v[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(q.first + rr / G) * a.q_stride +
-                                                               (size_t)(h * G + rr % G) * D + (i >> 10) * 64 + ch * 8);
-                }
+                for (int k = 0; k < NG; k++) {
+                    uint32_t o[16];
 #pragma unroll
-                for (int k = 0; k < N; k++) {
-                    const int i = tid + k * (kTileSoft * 32), ch = i & 7, r = (i >> 3) & (kTileRows - 1), g = i >> 10;
-                    v[k].x ^= flip; v[k].y ^= flip; v[k].z ^= flip; v[k].w ^= flip;
-                    *reinterpret_cast<uint4*>(gQ + g * (kTileRows * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) =
-                        make_uint4(__byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
-                                   __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
-                    const float2 f0 = h2f(v[k].x), f1 = h2f(v[k].y), f2 = h2f(v[k].z), f3 = h2f(v[k].w);
-                    float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                    if (ch == 0) s_qs[g][r] = sum;
+                    for (int e = 0; e < 4; e++) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (on) v = *reinterpret_cast<const uint4*>(qp + k * 32 + e * 8);
+                        v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+                        o[4 * e] = __byte_perm(v.x, v.z, 0x5410);
+                        o[4 * e + 1] = __byte_perm(v.x, v.z, 0x7632);
+                        o[4 * e + 2] = __byte_perm(v.y, v.w, 0x5410);
+                        o[4 * e + 3] = __byte_perm(v.y, v.w, 0x7632);
+                    }
+                    tmem_st16(t_row + Sh::kQ + half * (NG * 16) + k * 16, o);
                 }
-                fence_proxy_async_shared();
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_q);
-                named_bar(5, kTileSoft * 32);           // the rows' sums
             }
-            const uint32_t t_row = tmem + ((uint32_t)(32 * q4) << 16);
-            const int rr = min(rt * kTileRows + r, q.rows - 1);
+            const int rr = min(rt * kTileRows + r, sg.rows - 1);
             const int pos = p0 + rr / G, low = a.window > 0 ? pos - a.window + 1 : 0;
             const float sl2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-            float qs[NG], B[NG];
+            float poison[NG];                            // NaN where the row saw a V that is not finite
 #pragma unroll
-            for (int g = 0; g < NG; g++) {
-                qs[g] = s_qs[g][r];
-                B[g] = 0.f;
-            }
-            float m = -INFINITY, l = 0.f, unit = 0.f, vtop = 0.f;   // vtop: largest |scale| the unit admits
+            for (int g = 0; g < NG; g++) poison[g] = 0.f;
+            float m = -INFINITY, l = 0.f, vexp = 0.f;
             for (int t = 0; t < T; t++) {
                 const uint32_t n = gt + t;
-                const int slot = n % kTileSlots, st = n & 1;
-                const uint32_t t_s = t_row + Sh::kS + st * Sh::kStage;
-                if (ok) ok = __all_sync(0xffffffffu, fused_wait_bar(&b_full[slot], (n / kTileSlots) & 1u, c.stop) &&
-                                                         fused_wait_bar(&b_s[st], (n >> 1) & 1u, c.stop));
-                if (!ok) {                               // the others may still come to the barrier
-                    named_bar(1 + q4, 128);
+                const int st = n & 1;
+                const uint32_t t_s = t_row + Sh::kS + st * KT;
+                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_s[st], (n >> 1) & 1u, c.stop));
+                if (!ok) {                               // the other half may still come to the barrier
+                    named_bar(1 + q4, 64);
                     continue;
                 }
                 tc_fence_after();
-                const float4* sk = reinterpret_cast<const float4*>(gScale + (size_t)slot * 2 * NG * KT) + part * (HK / 2);
-                const float4* sv = sk + NG * KT / 2;
+                const TileMeta& meta = s_meta[n % kTileMeta];
                 float S[HK];
                 {
-                    uint32_t acc[NG][HK];
-#pragma unroll
-                    for (int g = 0; g < NG; g++)
-#pragma unroll
-                        for (int b = 0; b < HK / 8; b++) tmem_ld8_nw(t_s + g * KT + part * HK + b * 8, acc[g] + b * 8);
+                    uint32_t a0[16], a1[16];
+                    tmem_ld16_nw(t_s + half * HK, a0);
+                    tmem_ld16_nw(t_s + half * HK + 16, a1);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < HK; j++) S[j] = 0.f;
-#pragma unroll
-                    for (int g = 0; g < NG; g++)
-#pragma unroll
-                        for (int j = 0; j < HK / 2; j++) {
-                            const float4 f = sk[g * (KT / 2) + j];      // two entries
-                            S[2 * j] = fmaf(f.x, __uint_as_float(acc[g][2 * j]), fmaf(f.y, qs[g], S[2 * j]));
-                            S[2 * j + 1] = fmaf(f.z, __uint_as_float(acc[g][2 * j + 1]), fmaf(f.w, qs[g], S[2 * j + 1]));
-                        }
+                    for (int j = 0; j < 16; j++) {
+                        S[j] = __uint_as_float(a0[j]);
+                        S[16 + j] = __uint_as_float(a1[j]);
+                    }
                 }
-                const int j0 = (pg0 + t / Sh::kSub) * kKvPage + (t % Sh::kSub) * KT + part * HK;
-                const bool edge = j0 + HK - 1 > first_pos || j0 < last_low || !s_ok[slot];
+                const int j0 = (pg0 + t) * kKvPage + half * HK;
+                const bool edge = j0 + HK - 1 > first_pos || j0 < last_low || !meta.ok;
                 uint32_t vis = 0xFFFFFFFFu;
                 if (edge) {
                     vis = 0;
-                    const bool page = s_ok[slot] != 0;
+                    const bool page = meta.ok != 0;
 #pragma unroll
                     for (int j = 0; j < HK; j++) {
                         if (page && j0 + j <= pos && j0 + j >= low) vis |= 1u << j;
                         else S[j] = -INFINITY;
                     }
                 }
-                float top = S[0];
+                float tp[4] = {S[0], S[1], S[2], S[3]};
 #pragma unroll
-                for (int j = 1; j < HK; j++) top = fmaxf(top, S[j]);
-                s_mx[st][part][r] = top;
-                named_bar(1 + q4, 128);
-                top = fmaxf(fmaxf(s_mx[st][0][r], s_mx[st][1][r]), fmaxf(s_mx[st][2][r], s_mx[st][3][r])) * sl2;
-                // a scale of V beyond the present unit (alike in all threads)
-                const float* vm = s_vmax[slot];
-                const float vmax = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
-                float du = 0.f;
-                if (vmax > vtop && vmax < 1e30f) {
-                    du = fmaxf(fminf(3.f - floorf(log2f(vmax)), 60.f), -60.f) - unit;
-                    vtop = 127.f * exp2f(-(unit + du));
-                }
+                for (int j = 4; j < HK; j++) tp[j & 3] = fmaxf(tp[j & 3], S[j]);
+                float top = fmaxf(fmaxf(tp[0], tp[1]), fmaxf(tp[2], tp[3]));
+                s_mx[st][half][r] = top;
+                named_bar(1 + q4, 64);
+                const float sc = sl2 * meta.kinv;
+                top = fmaxf(top, s_mx[st][half ^ 1][r]) * sc;
+                const float du = meta.vexp - vexp;       // V's unit moved (alike in all threads)
                 const bool grow = top > m + 8.f;
                 if (__any_sync(0xffffffffu, grow) || du != 0.f) {
                     const float m2 = grow ? top : m;
-                    const float f = (m2 == -INFINITY ? 1.f : exp2_fast(m - m2)) * exp2f(du);
+                    const float fp = m2 == -INFINITY ? 1.f : exp2_fast(m - m2), f = fp * exp2f(du);
                     m = m2;
-                    unit += du;
-                    l *= f;
-#pragma unroll
-                    for (int g = 0; g < NG; g++) B[g] *= f;
-                    if (t > 0) {                         // O so far: this quarter's columns of the row
-                        ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1u, c.stop));
+                    vexp = meta.vexp;
+                    l *= fp;
+                    if (t > 0) {                         // O so far: this half's columns of the row
+                        ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(n - 1) % VR], ((n - 1) / VR) & 1u, c.stop));
                         if (!ok) continue;
                         tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < NG; k++) {
+                        for (int k = 0; k < NG * 2; k++) {
                             uint32_t o[16];
-                            const uint32_t at = t_row + Sh::kO + part * (NG * 16) + k * 16;
+                            const uint32_t at = t_row + Sh::kO + half * (NG * 32) + k * 16;
                             tmem_ld16_nw(at, o);
                             tmem_ld_wait();
 #pragma unroll
@@ -372,71 +410,57 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m - unit;
+                const float ref = m == -INFINITY ? 0.f : m - kTileLift;
+                const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int j = 0; j < HK; j++) S[j] = exp2_fast(fmaf(S[j], sl2, -ref));
-                float ls[4] = {S[0], S[1], S[2], S[3]};
+                for (int j = 0; j < HK; j += 2) {
+                    const float2 e = fma2(make_float2(S[j], S[j + 1]), sc2, ref2);
+                    S[j] = exp2_fast(e.x);
+                    S[j + 1] = exp2_fast(e.y);
+                    ls[(j >> 1) & 1] = add2(ls[(j >> 1) & 1], make_float2(S[j], S[j + 1]));
+                }
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                uint32_t P[16];
 #pragma unroll
-                for (int j = 4; j < HK; j++) ls[j & 3] += S[j];
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                const auto store = [&](auto some) {
-                    constexpr bool EDGE = decltype(some)::value;
+                for (int j = 0; j < 16; j++) P[j] = f2h(S[2 * j], S[2 * j + 1]);
+                tmem_st16(t_s + half * (HK / 2), P);
+                if (meta.any)
 #pragma unroll
-                    for (int g = 0; g < NG; g++) {
-                        uint32_t P[HK / 2];
-                        float b2[2] = {0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < HK / 2; j++) {
-                            const float4 f = sv[g * (KT / 2) + j];
-                            // an entry out of sight may hold a NaN scale
-                            const bool v0 = !EDGE || ((vis >> (2 * j)) & 1u), v1 = !EDGE || ((vis >> (2 * j + 1)) & 1u);
-                            P[j] = f2h(v0 ? S[2 * j] * f.x : 0.f, v1 ? S[2 * j + 1] * f.z : 0.f);
-                            if (v0) b2[0] = fmaf(S[2 * j], f.y, b2[0]);
-                            if (v1) b2[1] = fmaf(S[2 * j + 1], f.w, b2[1]);
-                        }
-                        B[g] += b2[0] + b2[1];
-                        const uint32_t at = t_s + g * (KT / 2) + part * (HK / 2);
-                        if (HK == 16) tmem_st8(at, P);
-                        else tmem_st4(at, P);
-                    }
-                };
-                if (edge) store(BoolC<true>{});
-                else store(BoolC<false>{});
+                    for (int g = 0; g < NG; g++)
+                        if (meta.bad[g][half] & vis) poison[g] = NAN;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_p[st]);
             }
-            // row sums of the four quarters, then this quarter's columns
-            s_sum[part][NG][r] = l;
+            // row sums of both halves, then this half's columns
+            s_sum[half][NG][r] = l;
 #pragma unroll
-            for (int g = 0; g < NG; g++) s_sum[part][g][r] = B[g];
-            named_bar(1 + q4, 128);
-            if (ok) ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(gt + T - 1) & 1], ((gt + T - 1) >> 1) & 1u, c.stop));
+            for (int g = 0; g < NG; g++) s_sum[half][g][r] = poison[g];
+            named_bar(1 + q4, 64);
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(gt + T - 1) % VR], ((gt + T - 1) / VR) & 1u, c.stop));
             tc_fence_after();
             if (ok) {
-                const float L = (s_sum[0][NG][r] + s_sum[1][NG][r]) + (s_sum[2][NG][r] + s_sum[3][NG][r]);
-                const float M = m == -INFINITY ? m : m - unit;
-                const bool whole = u == ie && ib >= blockIdx.x * per;
-                const bool row = rt * kTileRows + r < q.rows;
-                const int c0 = (int)(ib / per);
-                float* slot = x.part + (size_t)(2 * blockIdx.x + (c0 == (int)blockIdx.x ? 1 : 0)) * (kTileRows * (D + 2));
+                const float L = s_sum[0][NG][r] + s_sum[1][NG][r];
+                const float M = m == -INFINITY ? m : m - kTileLift;
+                const bool row = rt * kTileRows + r < sg.rows;
+                float* slot = x.part + (size_t)(2 * blockIdx.x + sg.slot) * (kTileRows * (D + 2));
                 const int head = h * G + rr % G;
-                const float f = L == 0.f ? 0.f : 1.f / L;
-                __half* out = a.out + (size_t)(q.first + rr / G) * a.out_stride + (size_t)head * D;
+                const float f = L == 0.f ? 0.f : 1.f / L, back = exp2f(-vexp);
+                __half* out = a.out + (size_t)(sg.first + rr / G) * a.out_stride + (size_t)head * D;
 #pragma unroll
-                for (int k = 0; k < NG; k++) {
-                    const int col = part * (NG * 16) + k * 16;
+                for (int k = 0; k < NG * 2; k++) {
+                    const int col = half * (NG * 32) + k * 16;
                     uint32_t o[16];
                     tmem_ld16_nw(t_row + Sh::kO + col, o);
                     tmem_ld_wait();
-                    const int g = col / 64;
-                    const float bb = (s_sum[0][g][r] + s_sum[1][g][r]) + (s_sum[2][g][r] + s_sum[3][g][r]);
+                    const float bad = s_sum[0][col / 64][r] + s_sum[1][col / 64][r];
                     if (!row) continue;
                     float v[16];
 #pragma unroll
-                    for (int e = 0; e < 16; e++) v[e] = __uint_as_float(o[e]) + bb;
-                    if (whole) {
+                    for (int e = 0; e < 16; e++) v[e] = fmaf(__uint_as_float(o[e]), back, bad);
+                    if (sg.whole) {
 #pragma unroll
                         for (int e = 0; e < 2; e++)
                             *reinterpret_cast<uint4*>(out + col + 8 * e) =
@@ -449,9 +473,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
-                if (part == 0 && row) {
-                    if (whole) {
-                        a.lse[(size_t)(q.first + rr / G) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                if (half == 0 && row) {
+                    if (sg.whole) {
+                        a.lse[(size_t)(sg.first + rr / G) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                     } else {
                         slot[kTileRows * D + r] = M;
                         slot[kTileRows * D + kTileRows + r] = L;
@@ -459,156 +483,270 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 }
             }
             tc_fence_before();
-        } else if (warp < kTileSoft + 4) {
-            // --------------------------------------------------- converters --
-            const int ct = tid - kTileSoft * 32, cw = warp - kTileSoft;
-            const int32_t* trow = c.table + (size_t)s * c.max_pages;
-            const int vw = ct & 7, vk = (ct >> 3) % (KT / 8), vg = (ct >> 3) / (KT / 8);   // V: 8 x 8 codes each
-            const int eg = ct / KT, ee = ct % KT;                                          // scale and bias of one entry
-            // a tile's raw bytes, two sets in turn: the next tile's loads are in flight while
-            // one is converted
+        TILE_SEGMENTS_END(sg)
+    } else if (warp < kTileSoft + kTileConv) {
+        // ------------------------------------------------------- converters --
+        reg_alloc<kTileConvRegs>();
+        TILE_SEGMENTS(seg, sg)
+            const int T = sg.T, h = sg.h, pg0 = sg.pg0;
+            constexpr int CT = kTileConv * 32, NK = (NG + 1) / 2;       // 128 NG pieces of K and of V a page
+            const int ct = tid - kTileSoft * 32;
+            const int32_t* trow = c.table + (size_t)sg.s * c.max_pages;
+            // a page's codes, two sets in turn: the next page's loads are in flight while one is
+            // converted
             struct Raw {
-                uint4 k[2];
-                uint32_t v[8], ks, vs;
-                bool page;
+                uint4 k[NK];                             // 32 codes of an entry
+                uint32_t v[NK][8];                       // a code word of 8 entries
             } raw[2];
             const auto page_at = [&](int t) {            // -1: behind the last entry
-                const int pg = pg0 + t / Sh::kSub;
-                return t < T && pg * kKvPage < q.len ? trow[pg] : -1;
+                const int pg = pg0 + t;
+                return t < T && pg * kKvPage < sg.len ? trow[pg] : -1;
             };
-            int id = page_at(0);                         // of the next tile to load, read one ahead
+            int id = page_at(0);                         // of the next page to load, read one ahead
             const auto load = [&](Raw& w, int t) {
-                w.page = (unsigned)id < (unsigned)c.n_pages;
-                if (!w.page) {
-                    if (ct == 0 && (pg0 + t / Sh::kSub) * kKvPage < q.len) kv_flag(c.status);
-                    w.k[0] = w.k[1] = make_uint4(0, 0, 0, 0);
+                // codes of a page that does not exist may be anything: its scales are zero
+                const size_t pg = (unsigned)id < (unsigned)c.n_pages ? id : 0;
+                const uint8_t* tile = c.pages + (pg * c.hkv + h) * (size_t)(4608 * NG);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) w.v[i] = 0;
-                    w.ks = w.vs = 0;
-                } else {
-                    const uint8_t* tile = c.pages + ((size_t)id * c.hkv + h) * (size_t)(4608 * NG);
-                    const int sub = (t % Sh::kSub) * KT;
+                for (int i = 0; i < NK; i++) {
+                    const int n = i * CT + ct;
+                    if (n < 128 * NG) {
+                        w.k[i] = __ldg(reinterpret_cast<const uint4*>(tile + n * 16));
+                        // piece of V: columns 8 vw + 4 (n & 1) .. of entries 8 vk ..
+                        const uint8_t* v = tile + 2304 * NG + (n >> 7) * 2048 + ((n >> 4) & 7) * 256 + ((n >> 1) & 7) * 4;
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const int n = i * 128 + ct, g = n / (KT * 2);
-                        if (g < NG)
-                            w.k[i] = __ldg(reinterpret_cast<const uint4*>(tile + g * 2048 + sub * 32 + (n % (KT * 2)) * 16));
-                    }
-                    if (vg < NG) {
-                        const uint8_t* v = tile + 2304 * NG + vg * 2048 + (sub + vk * 8) * 32 + vw * 4;
-#pragma unroll
-                        for (int i = 0; i < 8; i++) w.v[i] = __ldg(reinterpret_cast<const uint32_t*>(v + i * 32));
-                    }
-                    if (eg < NG) {
-                        const uint8_t* sp = tile + 2048 * NG + (eg * kKvPage + sub + ee) * 4;
-                        w.ks = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                        w.vs = __ldg(reinterpret_cast<const uint32_t*>(sp + 2304 * NG));
+                        for (int e = 0; e < 8; e++) w.v[i][e] = __ldg(reinterpret_cast<const uint32_t*>(v + e * 32));
                     }
                 }
                 id = page_at(t + 1);
             };
             const auto convert = [&](const Raw& w, int t) {
                 const uint32_t n = gt + t;
-                const int slot = n % kTileSlots;
-                // the slot's last user, P V of tile t - 3, has ended (tiles of earlier segments: all have)
-                if (t >= kTileSlots)
-                    ok = __all_sync(0xffffffffu, fused_wait_bar(&b_pv[(n - kTileSlots) & 1],
-                                                                ((n - kTileSlots) >> 1) & 1u, c.stop));
+                const int sl = n % kTileScales;
+                // the page's scales, and K's slot once Q K of the slot's last page has ended
+                if (ok)
+                    ok = __all_sync(0xffffffffu, wait_bar(&b_sc[sl], (n / kTileScales) & 1u, c.stop) &&
+                                                     (n < KR || wait_bar(&b_kf[n % KR], ((n / KR) - 1) & 1u, c.stop)));
                 if (!ok) return;
-                uint8_t* gk = gSlots + slot * Sh::kSlot;
-                uint8_t* gv = gk + Sh::kK;
+                uint8_t* gk = gK + (n % KR) * Sh::kK;
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int nn = i * 128 + ct, g = nn / (KT * 2), r = (nn >> 1) % KT, hf = nn & 1;
-                    if (g < NG) {
+                for (int i = 0; i < NK; i++) {
+                    const int nn = i * CT + ct, g = nn >> 7, r = (nn >> 1) & 63, hf = nn & 1;
+                    if (nn < 128 * NG) {
+                        const __half2 s2 = __half2half2(s_sc[sl][0][0][g][r]), b2 = __half2half2(s_sc[sl][0][1][g][r]);
+                        const float2 fs = __half22float2(s2), fb = __half22float2(b2);
                         const uint32_t word[4] = {w.k[i].x, w.k[i].y, w.k[i].z, w.k[i].w};
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            *reinterpret_cast<uint4*>(gk + g * (KT * 128) + r * 128 + (((hf * 4 + k) ^ (r & 7)) << 4)) =
-                                codes_centred(word[k]);
+                        for (int k = 0; k < 4; k++) {
+                            uint32_t cd[4], hi[4], lo[4];
+                            codes_exact(word[k], cd);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const __half2 hv = __hfma2(*reinterpret_cast<const __half2*>(&cd[e]), s2, b2);
+                                hi[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                                const float2 f = h2f(hi[e]), x2 = fma2(h2f(cd[e]), fs, fb);
+                                const float2 d = add2(x2, make_float2(-f.x, -f.y));
+                                lo[e] = f2h(d.x, d.y);
+                            }
+                            uint8_t* at = gk + g * (KT * 128) + r * 128 + (((hf * 4 + k) ^ (r & 7)) << 4);
+                            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(at + NG * KT * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
                     }
                 }
-                if (vg < NG) {
-#pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {     // columns 0..3, then 4..7 of the block
-                        uint4 e[4];                      // entries 2i, 2i + 1
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            e[i] = codes_centred(__byte_perm(w.v[2 * i], w.v[2 * i + 1], hf ? 0x7632 : 0x5410));
-                        uint8_t* dst = gv + vg * (64 * 128) + (8 * vw + 4 * hf) * 128;
-                        const int z = 4 * hf;
-                        *reinterpret_cast<uint4*>(dst + ((vk ^ z) << 4)) = make_uint4(e[0].x, e[1].x, e[2].x, e[3].x);
-                        *reinterpret_cast<uint4*>(dst + 128 + ((vk ^ (z + 1)) << 4)) = make_uint4(e[0].y, e[1].y, e[2].y, e[3].y);
-                        *reinterpret_cast<uint4*>(dst + 256 + ((vk ^ (z + 2)) << 4)) = make_uint4(e[0].z, e[1].z, e[2].z, e[3].z);
-                        *reinterpret_cast<uint4*>(dst + 384 + ((vk ^ (z + 3)) << 4)) = make_uint4(e[0].w, e[1].w, e[2].w, e[3].w);
-                    }
-                }
-                // scales: entries that no row of the tile sees count as zero, whatever they hold
-                float vm = 0.f;
-                if (eg < NG) {
-                    const int j = (pg0 + t / Sh::kSub) * kKvPage + (t % Sh::kSub) * KT + ee;
-                    const bool in = w.page && j <= last_pos && j >= first_low;
-                    const float2 fk = in ? h2f(w.ks) : make_float2(0.f, 0.f), fv = in ? h2f(w.vs) : make_float2(0.f, 0.f);
-                    float2* sc = gScale + (size_t)slot * 2 * NG * KT + eg * KT + ee;
-                    sc[0] = make_float2(fk.x, fmaf(8.f, fk.x, fk.y));
-                    sc[NG * KT] = make_float2(fv.x, fmaf(8.f, fv.x, fv.y));
-                    vm = fabsf(fv.x);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-                if (lane == 0) s_vmax[slot][cw] = vm;
-                if (ct == 0) s_ok[slot] = w.page;
                 fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b_full[slot]);
+                if (lane == 0) mbar_arrive(&b_k[n % KR]);
+                // V, transposed, once P V of the slot's last page has ended
+                if (n >= VR) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[n % VR], ((n / VR) - 1) & 1u, c.stop));
+                if (!ok) return;
+                uint8_t* gv = gV + (n % VR) * Sh::kV;
+#pragma unroll
+                for (int i = 0; i < NK; i++) {
+                    const int nn = i * CT + ct, g = nn >> 7, vk = (nn >> 4) & 7, vw = (nn >> 1) & 7, hf = nn & 1;
+                    if (nn < 128 * NG) {
+                        const uint4 sv = *reinterpret_cast<const uint4*>(&s_sc[sl][1][0][g][8 * vk]);
+                        const uint4 bv = *reinterpret_cast<const uint4*>(&s_sc[sl][1][1][g][8 * vk]);
+                        const uint32_t s2[4] = {sv.x, sv.y, sv.z, sv.w}, b2[4] = {bv.x, bv.y, bv.z, bv.w};
+                        uint32_t o[4][4];                // [column][entries 2e, 2e + 1]
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            uint32_t cd[4];
+                            codes_exact(__byte_perm(w.v[i][2 * e], w.v[i][2 * e + 1], hf ? 0x7632 : 0x5410), cd);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&cd[k]),
+                                                          *reinterpret_cast<const __half2*>(&s2[e]),
+                                                          *reinterpret_cast<const __half2*>(&b2[e]));
+                                o[k][e] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                        }
+                        uint8_t* dst = gv + g * (64 * 128) + (8 * vw + 4 * hf) * 128;
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            *reinterpret_cast<uint4*>(dst + k * 128 + ((vk ^ (4 * hf + k)) << 4)) =
+                                make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                    }
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&b_v[n % VR]);
+                    mbar_arrive(&b_scf[sl]);
+                }
             };
             load(raw[0], 0);
+            if (T > 1) load(raw[1], 1);
             for (int t = 0; ok && t < T; t += 2) {
-                if (t + 1 < T) load(raw[1], t + 1);
                 convert(raw[0], t);
                 if (t + 2 < T) load(raw[0], t + 2);
-                if (ok && t + 1 < T) convert(raw[1], t + 1);
+                if (t + 1 < T) convert(raw[1], t + 1);
+                if (t + 3 < T) load(raw[1], t + 3);
             }
-        } else if (lane == 0) {
-            // --------------------------------------------------- MMA issuer --
+        TILE_SEGMENTS_END(sg)
+    } else {
+        // ---------------------------------------------- MMA issuer and walker --
+        reg_dealloc<kTileIssueRegs>();
+        TILE_SEGMENTS(seg, sg)
+            const int T = sg.T;
+        if (warp == kTileSoft + kTileConv + 1) {
+            if (lane == 0) s_seg[(seg + 1) & 1] = walk.next(x);
+        } else if (warp > kTileSoft + kTileConv + 1) {
+            // ----------------------------------------------------- scales --
+            const int v = warp - (kTileSoft + kTileConv + 2);           // K, V
+            const int32_t* trow = c.table + (size_t)sg.s * c.max_pages;
+            const int last_pos = sg.p0 + (min((sg.rt + 1) * kTileRows, sg.rows) - 1) / G;
+            const int first_low = a.window > 0 ? sg.p0 + sg.rt * kTileRows / G - a.window + 1 : 0;
+            constexpr int N = 2 * NG;                                   // words a lane: entry 32 (i % 2) + lane of group i / 2
+            uint32_t w[2][N];
+            bool page[2];
+            const auto load = [&](uint32_t (&f)[N], bool& there, int t) {
+                const int pg = sg.pg0 + t;
+                const bool held = pg * kKvPage < sg.len;
+                const int id = held ? trow[pg] : -1;
+                there = (unsigned)id < (unsigned)c.n_pages;
+                if (held && !there && v == 0 && lane == 0) kv_flag(c.status);
+                const uint8_t* at = c.pages + ((size_t)(there ? id : 0) * c.hkv + sg.h) * (size_t)(4608 * NG) + (2304 * v + 2048) * NG;
+#pragma unroll
+                for (int i = 0; i < N; i++) f[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i * 32 + lane);
+            };
+            int vexp = 0;                                // log2 of V's factor
+            float vtop = 0.f;                            // largest value it admits
+            const auto scales = [&](const uint32_t (&f)[N], bool there, int t) {
+                const uint32_t n = gt + t;
+                const int sl = n % kTileScales;
+                TileMeta& meta = s_meta[n % kTileMeta];
+                const int j = (sg.pg0 + t) * kKvPage + lane;
+                const bool in0 = there && j <= last_pos && j >= first_low;
+                const bool in1 = there && j + 32 <= last_pos && j + 32 >= first_low;
+                float mx = 0.f;
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    const float2 x2 = h2f(f[i]);
+                    const bool in = i & 1 ? in1 : in0, fin = fabsf(x2.x) <= 65504.f && fabsf(x2.y) <= 65504.f;
+                    if (in && fin) mx = fmaxf(mx, fmaf(15.f, fabsf(x2.x), fabsf(x2.y)));
+                    if (in && !fin) bad |= 1u << i;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                // K: the page's largest value to 2^13..2^14.  V: the first to 2^10..2^11, and anew
+                // when a page exceeds 2^15
+                int e;
+                if (v == 0) {
+                    e = mx > 0.f ? 13 - exponent_of(mx) : 0;
+                } else {
+                    if (mx > vtop) {
+                        vexp = 10 - exponent_of(mx);
+                        vtop = 32768.f * pow2(-vexp);
+                    }
+                    e = vexp;
+                }
+                if (n >= kTileScales)
+                    ok = __all_sync(0xffffffffu, wait_bar(&b_scf[sl], ((n / kTileScales) - 1) & 1u, c.stop));
+                if (!ok) return;
+                const float up = pow2(e);
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    const float2 x2 = h2f(f[i]);
+                    // entries that no row of the tile sees count as zero, whatever they hold, and
+                    // values of V that are not finite too (their rows learn of them)
+                    const bool take = (i & 1 ? in1 : in0) && !(v == 1 && ((bad >> i) & 1u));
+                    s_sc[sl][v][0][i >> 1][32 * (i & 1) + lane] = __float2half_rn(take ? x2.x * up : 0.f);
+                    s_sc[sl][v][1][i >> 1][32 * (i & 1) + lane] = __float2half_rn(take ? x2.y * up : 0.f);
+                    if (v == 1) {
+                        const uint32_t word = __ballot_sync(0xffffffffu, (bad >> i) & 1u);
+                        any = any || word;
+                        if (lane == 0) meta.bad[i >> 1][i & 1] = word;
+                    }
+                }
+                if (lane == 0) {
+                    if (v == 0) {
+                        meta.kinv = pow2(-e);
+                        meta.ok = there;
+                    } else {
+                        meta.vexp = (float)e;
+                        meta.any = any;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_sc[sl]);
+            };
+            load(w[0], page[0], 0);
+            if (T > 1) load(w[1], page[1], 1);
+            for (int t = 0; ok && t < T; t += 2) {
+                scales(w[0], page[0], t);
+                if (t + 2 < T) load(w[0], page[0], t + 2);
+                if (ok && t + 1 < T) scales(w[1], page[1], t + 1);
+                if (t + 3 < T) load(w[1], page[1], t + 3);
+            }
+        } else if (warp == kTileSoft + kTileConv && lane == 0) {
             constexpr uint32_t id_s = kTcIdescF16 | ((uint32_t)(KT >> 3) << 17);
-            constexpr uint32_t id_o = kTcIdescF16 | (8u << 17);
-            const uint64_t dq = tc_sdesc_sw128(sQ);
+            constexpr uint32_t id_o = kTcIdescF16 | ((uint32_t)(D >> 3) << 17);
+            // descriptors: the high half is the same for all, the low half (address) moves
+            const uint32_t dhi = (uint32_t)(tc_sdesc_sw128(0) >> 32);
             const auto pv = [&](int t) {
                 const uint32_t n = gt + t;
-                const int slot = n % kTileSlots, st = n & 1;
-                if (!fused_wait_bar(&b_p[st], (n >> 1) & 1u, c.stop)) return false;
+                const int st = n & 1;
+                if (!wait_bar(&b_v[n % VR], (n / VR) & 1u, c.stop) ||
+                    !wait_bar(&b_p[st], (n >> 1) & 1u, c.stop))
+                    return false;
                 tc_fence_after();
-                const uint64_t dv = tc_sdesc_sw128(sSlots + slot * Sh::kSlot + Sh::kK);
+                const uint32_t dv = (uint32_t)tc_sdesc_sw128(sV + (n % VR) * Sh::kV), pa = tmem + Sh::kS + st * KT;
+                tc_mma_ts(tmem + Sh::kO, pa, tc_desc(dv, dhi), id_o, t > 0 ? 1u : 0u);
 #pragma unroll
-                for (int g = 0; g < NG; g++)
-#pragma unroll
-                    for (int k = 0; k < KT / 16; k++)
-                        tc_mma_ts(tmem + Sh::kO + g * 64, tmem + Sh::kS + st * Sh::kStage + g * (KT / 2) + 8 * k,
-                                  dv + (uint64_t)((g * 64 * 128) >> 4) + 2u * k, id_o, t > 0 || k > 0 ? 1u : 0u);
-                mma_commit(&b_pv[st]);
+                for (int k = 1; k < KT / 16; k++) tc_mma_ts_acc(tmem + Sh::kO, pa + 8 * k, tc_desc(dv + 2u * k, dhi), id_o);
+                mma_commit(&b_pv[n % VR]);
                 return true;
             };
-            if (!fused_wait_bar(&b_q, seg & 1u, c.stop)) ok = false;
+            if (!wait_bar(&b_q, seg & 1u, c.stop)) ok = false;
             int done = 0, asked = 0;                     // tiles whose P V and whose Q K have been issued
             for (int t = 0; ok && t < T; t++) {
                 const uint32_t n = gt + t;
-                const int slot = n % kTileSlots, st = n & 1;
-                if (!fused_wait_bar(&b_full[slot], (n / kTileSlots) & 1u, c.stop) ||
+                const int st = n & 1;
+                if (!wait_bar(&b_k[n % KR], (n / KR) & 1u, c.stop) ||
                     // the stage's P of tile t - 2 has been used
-                    (t >= 2 && !fused_wait_bar(&b_pv[st], ((n - 2) >> 1) & 1u, c.stop))) {
+                    (t >= 2 && !wait_bar(&b_pv[(n - 2) % VR], ((n - 2) / VR) & 1u, c.stop))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t dk = tc_sdesc_sw128(sSlots + slot * Sh::kSlot);
+                const uint32_t dk = (uint32_t)tc_sdesc_sw128(sK + (n % KR) * Sh::kK), ds = tmem + Sh::kS + st * KT;
 #pragma unroll
-                for (int g = 0; g < NG; g++)
+                for (int z = 0; z < 2; z++)              // hi, lo
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        tc_mma_ss(tmem + Sh::kS + st * Sh::kStage + g * KT, dq + (uint64_t)((g * kTileRows * 128) >> 4) + 2u * k,
-                                  dk + (uint64_t)((g * KT * 128) >> 4) + 2u * k, id_s, k > 0 ? 1u : 0u);
+                    for (int g = 0; g < NG; g++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const uint32_t da = tmem + Sh::kQ + g * 32 + 8 * k;
+                            const uint64_t db = tc_desc(dk + (((z * NG + g) * KT * 128) >> 4) + 2u * k, dhi);
+                            if (z + g + k == 0) tc_mma_ts(ds, da, db, id_s, 0u);
+                            else tc_mma_ts_acc(ds, da, db, id_s);
+                        }
                 mma_commit(&b_s[st]);
+                mma_commit(&b_kf[n % KR]);
+                mbar_arrive(&b_s[st]);
                 asked = t + 1;
                 if (t > 0) {
                     if (!pv(t - 1)) { ok = false; break; }
@@ -618,22 +756,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             if (ok && !pv(T - 1)) ok = false;
             else if (ok) done = T;
             // every commit has arrived before the segment ends
-            if (done > 0) mma_drain_wait(&b_pv[(gt + done - 1) & 1], ((gt + done - 1) >> 1) & 1u);
-            if (!ok && asked > 0) mma_drain_wait(&b_s[(gt + asked - 1) & 1], ((gt + asked - 1) >> 1) & 1u);
+            if (done > 0) mma_drain_wait(&b_pv[(gt + done - 1) % VR], ((gt + done - 1) / VR) & 1u);
+            if (!ok && asked > 0) mma_drain_wait(&b_kf[(gt + asked - 1) % KR], ((gt + asked - 1) / KR) & 1u);
         }
-        gt += T;
-        seg++;
-        if (ib >= blockIdx.x * per && u < ie) {         // the item goes on in the next CTA
-            cut = true;
-            if (tid == 0) x.cut[blockIdx.x] = TileCut{(int)((ie - 1) / per) - (int)blockIdx.x + 1, q.first, q.rows, rt, h};
-        }
-        // a role that gave up has recorded it: all leave together; shared memory is free then
-        if (__syncthreads_or(!ok)) {
-            cut = false;
-            break;
-        }
+        TILE_SEGMENTS_END(sg)
     }
-    if (tid == 0 && !cut) x.cut[blockIdx.x].parts = 0;
+#undef TILE_SEGMENTS
+#undef TILE_SEGMENTS_END
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {

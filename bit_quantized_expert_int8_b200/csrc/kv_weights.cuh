@@ -52,8 +52,9 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
     using Sh = WtShape<NG>;
     constexpr int D = Sh::kD, SETS = Sh::kSets, UNIT = Sh::kUnit;
     extern __shared__ __align__(128) uint8_t wt_smem[];
-    __shared__ float s_qs[kWtBlock / 8][NG][8], s_lse[kWtBlock];
-    __shared__ int s_pos[kWtBlock];
+    __shared__ __align__(16) float s_qs[kWtBlock / 8][NG][8];
+    __shared__ __align__(16) float s_lse[kWtBlock];
+    __shared__ __align__(16) int s_pos[kWtBlock];
     __shared__ long long s_total, s_base0;
     __shared__ int s_seq;
     const KvArgs& c = a.c;

@@ -40,4 +40,29 @@ __device__ __forceinline__ bool fused_wait_bar(uint64_t* bar, uint32_t parity, i
     }
 }
 
+// The same for kernels whose warps wait often beside others that work: the
+// hardware suspends the thread up to a microsecond at a time, where polling would
+// take issue slots from the working warps.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
+    if (mbar_try_wait_long(bar, parity)) return true;
+    const unsigned long long t0 = gtimer_ns();
+    while (!mbar_try_wait_long(bar, parity)) {
+        const unsigned long long el = gtimer_ns() - t0;
+        if (el > kWaitNs) { fused_fail(status); return false; }
+        if (el > kAbortCheckNs && fused_aborted(status)) return false;
+    }
+    return true;
+}
+
 }  // namespace moeq4
