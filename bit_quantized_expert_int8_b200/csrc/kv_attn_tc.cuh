@@ -25,7 +25,7 @@
 //                 and half w / 4 of its entries; the halves of a row exchange
 //                 their maximum through shared memory.  They bring Q to tensor memory.
 //   warps 8..15   converters: codes from global memory (the next page's loads in
-//                 flight while one is converted) to fp16 operands in shared memory,
+//                 flight while this one is converted) to fp16 operands in shared memory,
 //                 128-byte swizzle: K entry-major, V transposed (8 x 4 blocks of
 //                 codes turned in registers);
 //   warp 16       MMA issuer (one thread): Q K of tile t + 1 is issued before P V of
@@ -492,42 +492,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             constexpr int CT = kTileConv * 32, NK = (NG + 1) / 2;       // 128 NG pieces of K and of V a page
             const int ct = tid - kTileSoft * 32;
             const int32_t* trow = c.table + (size_t)sg.s * c.max_pages;
-            // a page's codes, two sets in turn: the next page's loads are in flight while one is
-            // converted
-            struct Raw {
-                uint4 k[NK];                             // 32 codes of an entry
-                uint32_t v[NK][8];                       // a code word of 8 entries
-            } raw[2];
+            // a page's codes; those of the next page are loaded as soon as a part has been
+            // converted, so K's come while V is converted and V's while K is
+            uint4 rk[NK];                                // 32 codes of an entry
+            uint32_t rv[NK][8];                          // a code word of 8 entries
             const auto page_at = [&](int t) {            // -1: behind the last entry
                 const int pg = pg0 + t;
                 return t < T && pg * kKvPage < sg.len ? trow[pg] : -1;
             };
-            int id = page_at(0);                         // of the next page to load, read one ahead
-            const auto load = [&](Raw& w, int t) {
-                // codes of a page that does not exist may be anything: its scales are zero
-                const size_t pg = (unsigned)id < (unsigned)c.n_pages ? id : 0;
-                const uint8_t* tile = c.pages + (pg * c.hkv + h) * (size_t)(4608 * NG);
+            // codes of a page that does not exist may be anything: its scales are zero
+            const auto tile_at = [&](int id) {
+                return c.pages + ((size_t)((unsigned)id < (unsigned)c.n_pages ? id : 0) * c.hkv + h) * (size_t)(4608 * NG);
+            };
+            const auto load_k = [&](const uint8_t* tile) {
+#pragma unroll
+                for (int i = 0; i < NK; i++)
+                    if (i * CT + ct < 128 * NG) rk[i] = __ldg(reinterpret_cast<const uint4*>(tile) + i * CT + ct);
+            };
+            const auto load_v = [&](const uint8_t* tile) {
 #pragma unroll
                 for (int i = 0; i < NK; i++) {
-                    const int n = i * CT + ct;
-                    if (n < 128 * NG) {
-                        w.k[i] = __ldg(reinterpret_cast<const uint4*>(tile + n * 16));
-                        // piece of V: columns 8 vw + 4 (n & 1) .. of entries 8 vk ..
-                        const uint8_t* v = tile + 2304 * NG + (n >> 7) * 2048 + ((n >> 4) & 7) * 256 + ((n >> 1) & 7) * 4;
+                    const int n = i * CT + ct;           // columns 8 vw + 4 (n & 1) .. of entries 8 vk ..
+                    const uint8_t* v = tile + 2304 * NG + (n >> 7) * 2048 + ((n >> 4) & 7) * 256 + ((n >> 1) & 7) * 4;
+                    if (n < 128 * NG)
 #pragma unroll
-                        for (int e = 0; e < 8; e++) w.v[i][e] = __ldg(reinterpret_cast<const uint32_t*>(v + e * 32));
-                    }
+                        for (int e = 0; e < 8; e++) rv[i][e] = __ldg(reinterpret_cast<const uint32_t*>(v + e * 32));
                 }
-                id = page_at(t + 1);
             };
-            const auto convert = [&](const Raw& w, int t) {
+            int id = page_at(0), id2 = page_at(1);       // pages t and t + 1
+            load_k(tile_at(id));
+            load_v(tile_at(id));
+            for (int t = 0; t < T; t++) {
                 const uint32_t n = gt + t;
                 const int sl = n % kTileScales;
                 // the page's scales, and K's slot once Q K of the slot's last page has ended
                 if (ok)
                     ok = __all_sync(0xffffffffu, wait_bar(&b_sc[sl], (n / kTileScales) & 1u, c.stop) &&
                                                      (n < KR || wait_bar(&b_kf[n % KR], ((n / KR) - 1) & 1u, c.stop)));
-                if (!ok) return;
+                if (!ok) break;
                 uint8_t* gk = gK + (n % KR) * Sh::kK;
 #pragma unroll
                 for (int i = 0; i < NK; i++) {
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     if (nn < 128 * NG) {
                         const __half2 s2 = __half2half2(s_sc[sl][0][0][g][r]), b2 = __half2half2(s_sc[sl][0][1][g][r]);
                         const float2 fs = __half22float2(s2), fb = __half22float2(b2);
-                        const uint32_t word[4] = {w.k[i].x, w.k[i].y, w.k[i].z, w.k[i].w};
+                        const uint32_t word[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             uint32_t cd[4], hi[4], lo[4];
@@ -557,9 +559,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_k[n % KR]);
+                id = id2;
+                id2 = page_at(t + 2);
+                const uint8_t* next = tile_at(id);
+                if (t + 1 < T) load_k(next);
                 // V, transposed, once P V of the slot's last page has ended
                 if (n >= VR) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[n % VR], ((n / VR) - 1) & 1u, c.stop));
-                if (!ok) return;
+                if (!ok) break;
                 uint8_t* gv = gV + (n % VR) * Sh::kV;
 #pragma unroll
                 for (int i = 0; i < NK; i++) {
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
                             uint32_t cd[4];
-                            codes_exact(__byte_perm(w.v[i][2 * e], w.v[i][2 * e + 1], hf ? 0x7632 : 0x5410), cd);
+                            codes_exact(__byte_perm(rv[i][2 * e], rv[i][2 * e + 1], hf ? 0x7632 : 0x5410), cd);
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&cd[k]),
@@ -594,14 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     mbar_arrive(&b_v[n % VR]);
                     mbar_arrive(&b_scf[sl]);
                 }
-            };
-            load(raw[0], 0);
-            if (T > 1) load(raw[1], 1);
-            for (int t = 0; ok && t < T; t += 2) {
-                convert(raw[0], t);
-                if (t + 2 < T) load(raw[0], t + 2);
-                if (t + 1 < T) convert(raw[1], t + 1);
-                if (t + 3 < T) load(raw[1], t + 3);
+                if (t + 1 < T) load_v(next);
             }
         TILE_SEGMENTS_END(sg)
     } else {
@@ -618,9 +617,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             const int last_pos = sg.p0 + (min((sg.rt + 1) * kTileRows, sg.rows) - 1) / G;
             const int first_low = a.window > 0 ? sg.p0 + sg.rt * kTileRows / G - a.window + 1 : 0;
             constexpr int N = 2 * NG;                                   // words a lane: entry 32 (i % 2) + lane of group i / 2
-            uint32_t w[2][N];
-            bool page[2];
-            const auto load = [&](uint32_t (&f)[N], bool& there, int t) {
+            uint32_t f[N];
+            bool there = false;
+            const auto load = [&](int t) {
                 const int pg = sg.pg0 + t;
                 const bool held = pg * kKvPage < sg.len;
                 const int id = held ? trow[pg] : -1;
@@ -632,7 +631,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             };
             int vexp = 0;                                // log2 of V's factor
             float vtop = 0.f;                            // largest value it admits
-            const auto scales = [&](const uint32_t (&f)[N], bool there, int t) {
+            load(0);
+            for (int t = 0; t < T; t++) {
                 const uint32_t n = gt + t;
                 const int sl = n % kTileScales;
                 TileMeta& meta = s_meta[n % kTileMeta];
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 }
                 if (n >= kTileScales)
                     ok = __all_sync(0xffffffffu, wait_bar(&b_scf[sl], ((n / kTileScales) - 1) & 1u, c.stop));
-                if (!ok) return;
+                if (!ok) break;
                 const float up = pow2(e);
                 bool any = false;
 #pragma unroll
@@ -692,14 +692,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_sc[sl]);
-            };
-            load(w[0], page[0], 0);
-            if (T > 1) load(w[1], page[1], 1);
-            for (int t = 0; ok && t < T; t += 2) {
-                scales(w[0], page[0], t);
-                if (t + 2 < T) load(w[0], page[0], t + 2);
-                if (ok && t + 1 < T) scales(w[1], page[1], t + 1);
-                if (t + 3 < T) load(w[1], page[1], t + 3);
+                if (t + 1 < T) load(t + 1);
             }
         } else if (warp == kTileSoft + kTileConv && lane == 0) {
             constexpr uint32_t id_s = kTcIdescF16 | ((uint32_t)(KT >> 3) << 17);
