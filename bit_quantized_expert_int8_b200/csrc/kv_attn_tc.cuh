@@ -50,9 +50,9 @@ constexpr int kTileSoft = 8;           // softmax warps: 2 per 32 rows
 constexpr int kTileConv = 8;           // converter warps
 constexpr int kTileWarps = kTileSoft + kTileConv + 4;    // the issuer's warpgroup: one warp works
 // Registers: 96 a thread at launch (640 threads); the issuer's warpgroup gives some of
-// its own up to the converters: 256 x 96 + 256 x 120 + 128 x 48 <= 640 x 96.
-constexpr int kTileConvRegs = 120, kTileIssueRegs = 48;
-static_assert((kTileSoft * 96 + kTileConv * kTileConvRegs + 4 * kTileIssueRegs) <= kTileWarps * 96, "registers");
+// its own up to the others: 256 x 112 + 256 x 104 + 128 x 48 = 640 x 96.
+constexpr int kTileSoftRegs = 112, kTileConvRegs = 104, kTileIssueRegs = 48;
+static_assert((kTileSoft * kTileSoftRegs + kTileConv * kTileConvRegs + 4 * kTileIssueRegs) <= kTileWarps * 96, "registers");
 constexpr int kTileThreads = kTileWarps * 32;
 constexpr int kTileItemCost = 4;       // pages an item costs beside its own
 constexpr int kTileMinUnits = 6;       // pages per CTA at least
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 
     if (warp < kTileSoft) {
         // ---------------------------------------------------------- softmax --
+        reg_alloc<kTileSoftRegs>();
         TILE_SEGMENTS(seg, sg)
             const int T = sg.T, rt = sg.rt, h = sg.h, p0 = sg.p0, pg0 = sg.pg0;
             const int first_pos = p0 + rt * kTileRows / G;      // least and greatest row
