@@ -112,10 +112,16 @@ struct WtKernel {
     WtFn fn;
     int smem;
 };
-static WtKernel weights_kernel(int ng) {
-    static const WtKernel table[4] = {{k_attn_weights<1>, WtShape<1>::kSmem}, {k_attn_weights<2>, WtShape<2>::kSmem},
-                                      {k_attn_weights<3>, WtShape<3>::kSmem}, {k_attn_weights<4>, WtShape<4>::kSmem}};
-    return table[ng - 1];
+template <int NG, bool MANY>
+static WtKernel weights_of() {
+    return {k_attn_weights<NG, MANY>, WtShape<NG, MANY>::kSmem};
+}
+static WtKernel weights_kernel(int ng, bool many) {
+    static const WtKernel table[4][2] = {{weights_of<1, false>(), weights_of<1, true>()},
+                                         {weights_of<2, false>(), weights_of<2, true>()},
+                                         {weights_of<3, false>(), weights_of<3, true>()},
+                                         {weights_of<4, false>(), weights_of<4, true>()}};
+    return table[ng - 1][many];
 }
 static SplitKernel split_kernel(int ng, int rt) {
     static const SplitKernel table[4][2] = {{split_of<1, 1>(), split_of<1, 2>()},
@@ -206,8 +212,10 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     const size_t o_count = take(ctas * sizeof(int));
     kv->counts = ctas;
     const size_t o_cut = take((size_t)kv->n_sms * sizeof(TileCut));
-    const WtKernel wt = weights_kernel(cfg->head_dim / 64);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(wt.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, wt.smem);
+    for (int many = 0; many < 2; many++) {
+        const WtKernel k = weights_kernel(cfg->head_dim / 64, many);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    }
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
     if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictSmem);
@@ -378,7 +386,7 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
                         kv->split_smem[rt - 1], stream, x));
     }
     if (flags & MOE_ATTN_WEIGHTS) {
-        const WtKernel k = weights_kernel(a.c.ng);
+        const WtKernel k = weights_kernel(a.c.ng, most > kWtBlock);
         KV_CK(kv_launch(1, k.fn, dim3(2 * kv->n_sms), kWtThreads, k.smem, stream, a));
     }
     return MOE_OK;

@@ -11,8 +11,12 @@
 // written by one thread: the result does not depend on the order in which CTAs
 // run.  With few rows the kernel is bound by reading K, with many by the fold of
 // the groups' sums (S = sum_g s_g q_g . (c_g - 8) + (b_g + 8 s_g) sum(q_g)) and the
-// exponentials.  A unit is what the eight warps of a CTA hold at once; CTAs take
-// equal runs of units, over all sequences and kv heads.
+// exponentials.  A unit is what the eight warps of a CTA hold at once: 256 entries
+// (128 with wide heads) when rows are few; 64 when there are many (MANY), each 16
+// held by two warps that take every second 8 rows and add up at the end, because
+// the entries alone do not fill the device (256 rows over 2,900 entries: 96 units of
+// 256, 127 us; 368 of 64).  CTAs take equal runs of units, over all sequences and kv
+// heads.
 #pragma once
 #include "kv_attn.cuh"
 
@@ -22,11 +26,13 @@ constexpr int kWtWarps = 8;
 constexpr int kWtThreads = kWtWarps * 32;
 constexpr int kWtBlock = 64;           // query rows in shared memory
 
-template <int NG>
+template <int NG, bool MANY>
 struct WtShape {
     static constexpr int kD = 64 * NG;
-    static constexpr int kSets = NG <= 2 ? 2 : 1;               // 16 entries each, per warp
-    static constexpr int kUnit = kWtWarps * 16 * kSets;         // entries a CTA holds: 4 or 2 pages
+    static constexpr int kSets = NG <= 2 && !MANY ? 2 : 1;      // 16 entries each, per warp
+    static constexpr int kGroups = MANY ? 4 : 8;                // warps with entries of their own
+    static constexpr int kSplit = kWtWarps / kGroups;           // warps that share the rows of the same entries
+    static constexpr int kUnit = kGroups * 16 * kSets;          // entries a CTA holds: 4, 2 or 1 pages
     static constexpr int kQ = NG * 2 * 32 * 16;                 // operands of 8 query rows, bytes
     static constexpr int kSmem = kWtBlock / 8 * kQ;
 };
@@ -47,14 +53,15 @@ __device__ __forceinline__ WtSeq wt_seq(const AttnArgs& a, int s) {
     return q;
 }
 
-template <int NG>
+template <int NG, bool MANY>
 __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a) {
-    using Sh = WtShape<NG>;
+    using Sh = WtShape<NG, MANY>;
     constexpr int D = Sh::kD, SETS = Sh::kSets, UNIT = Sh::kUnit;
     extern __shared__ __align__(128) uint8_t wt_smem[];
     __shared__ __align__(16) float s_qs[kWtBlock / 8][NG][8];
     __shared__ __align__(16) float s_lse[kWtBlock];
     __shared__ __align__(16) int s_pos[kWtBlock];
+    __shared__ float s_part[kWtWarps][16];
     __shared__ long long s_total, s_base0;
     __shared__ int s_seq;
     const KvArgs& c = a.c;
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
         }
         const int h = (int)((u - base) / q.units);
         const int e0 = q.lo + (int)((u - base) % q.units) * UNIT;        // first entry of the unit
-        const int j0 = e0 + warp * (16 * SETS);                          // of this warp
+        const int j0 = e0 + warp % Sh::kGroups * (16 * SETS);            // of this warp
         const int p0 = q.len - q.n, rows = q.n * G;
         // this warp's entries lie in one page
         const int pg = j0 / kKvPage;
@@ -166,6 +173,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
                 const int t = tid & 3, r = tid >> 2, rr = blk * kWtBlock + r;
                 const bool on = rr < rows;
                 const int row = q.first + min(rr, rows - 1) / G, head = h * G + min(rr, rows - 1) % G;
+                const float lse_now = t == 0 && on ? a.lse[(size_t)row * c.hq + head] : -INFINITY;
 #pragma unroll
                 for (int g = 0; g < NG; g++) {
                     uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
@@ -192,8 +200,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
                     if (t == 0) s_qs[r >> 3][g][r & 7] = qsum;
                 }
                 if (t == 0) {
-                    const float v = on ? a.lse[(size_t)row * c.hq + head] : -INFINITY;
-                    s_lse[r] = v == -INFINITY ? INFINITY : v * kLog2e;   // such rows add nothing
+                    s_lse[r] = lse_now == -INFINITY ? INFINITY : lse_now * kLog2e;   // such rows add nothing
                     s_pos[r] = p0 + min(rr, rows - 1) / G;
                 }
                 s_now = s;
@@ -203,56 +210,80 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
             }
             if (!in) continue;
             const int tiles = min(kWtBlock, rows - blk * kWtBlock + 7) / 8;
-            for (int rt = 0; rt < tiles; rt++) {
-                const int r0 = rt * 8, r7 = min(r0 + 7, rows - 1 - blk * kWtBlock);
-                const int pmin = s_pos[r0], pmax = s_pos[r7];
+            // PAIR row tiles side by side: their products and exponentials hide each other's latency
+            constexpr int PAIR = MANY ? 2 : 1;
+            for (int rt0 = warp / Sh::kGroups * PAIR; rt0 < tiles; rt0 += Sh::kSplit * PAIR) {
+                const int r0 = rt0 * 8, r1 = min(r0 + 8 * PAIR, rows - blk * kWtBlock) - 1;
+                const int pmin = s_pos[r0], pmax = s_pos[r1];
                 if (pmax < j0) continue;                                 // all before these entries
                 if (a.window > 0 && pmin - a.window + 1 > j0 + 16 * SETS - 1) continue;
                 const bool edge = j0 + 16 * SETS - 1 > pmin || (a.window > 0 && j0 < pmax - a.window + 1);
-                float S[SETS][4];
+                float S[PAIR][SETS][4];
 #pragma unroll
-                for (int z = 0; z < SETS; z++)
+                for (int y = 0; y < PAIR; y++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++) S[z][k] = 0.f;
+                    for (int z = 0; z < SETS; z++)
 #pragma unroll
-                for (int g = 0; g < NG; g++) {
-                    const uint4 b0 = lds128(qb + rt * Sh::kQ + ((g * 2) * 32 + lane) * 16);
-                    const uint4 b1 = lds128(qb + rt * Sh::kQ + ((g * 2 + 1) * 32 + lane) * 16);
-                    const float2 qs = *reinterpret_cast<const float2*>(&s_qs[rt][g][2 * t4]);
+                        for (int k = 0; k < 4; k++) S[y][z][k] = 0.f;
 #pragma unroll
-                    for (int z = 0; z < SETS; z++) {
-                        const uint32_t(&k)[4][4] = kf[z][g];
-                        float d[4];
-                        mma_f16(d, k[0][0], k[0][1], k[0][2], k[0][3], b0.x, b0.y, 0.f, 0.f, 0.f, 0.f);
-                        mma_f16(d, k[1][0], k[1][1], k[1][2], k[1][3], b0.z, b0.w);
-                        mma_f16(d, k[2][0], k[2][1], k[2][2], k[2][3], b1.x, b1.y);
-                        mma_f16(d, k[3][0], k[3][1], k[3][2], k[3][3], b1.z, b1.w);
-                        const float2 f0 = sb[z][g][0], f1 = sb[z][g][1];
-                        S[z][0] = fmaf(f0.x, d[0], fmaf(f0.y, qs.x, S[z][0]));
-                        S[z][1] = fmaf(f0.x, d[1], fmaf(f0.y, qs.y, S[z][1]));
-                        S[z][2] = fmaf(f1.x, d[2], fmaf(f1.y, qs.x, S[z][2]));
-                        S[z][3] = fmaf(f1.x, d[3], fmaf(f1.y, qs.y, S[z][3]));
-                    }
-                }
-                const float2 lse = *reinterpret_cast<const float2*>(&s_lse[r0 + 2 * t4]);
+                for (int g = 0; g < NG; g++)
 #pragma unroll
-                for (int z = 0; z < SETS; z++) {
-                    float w[4] = {exp2_fast(fmaf(S[z][0], sl2, -lse.x)), exp2_fast(fmaf(S[z][1], sl2, -lse.y)),
-                                  exp2_fast(fmaf(S[z][2], sl2, -lse.x)), exp2_fast(fmaf(S[z][3], sl2, -lse.y))};
-                    if (edge) {
-                        const int2 p = *reinterpret_cast<const int2*>(&s_pos[r0 + 2 * t4]);
+                    for (int y = 0; y < PAIR; y++) {
+                        // rows behind the block's last are zero there, and add nothing
+                        const uint4 b0 = lds128(qb + (rt0 + y) * Sh::kQ + ((g * 2) * 32 + lane) * 16);
+                        const uint4 b1 = lds128(qb + (rt0 + y) * Sh::kQ + ((g * 2 + 1) * 32 + lane) * 16);
+                        const float2 qs = *reinterpret_cast<const float2*>(&s_qs[rt0 + y][g][2 * t4]);
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const int j = j0 + 16 * z + 8 * (k >> 1) + g8, at = k & 1 ? p.y : p.x;
-                            if (j > at || (a.window > 0 && j <= at - a.window)) w[k] = 0.f;
+                        for (int z = 0; z < SETS; z++) {
+                            const uint32_t(&k)[4][4] = kf[z][g];
+                            float(&S4)[4] = S[y][z];
+                            float d[4];
+                            mma_f16(d, k[0][0], k[0][1], k[0][2], k[0][3], b0.x, b0.y, 0.f, 0.f, 0.f, 0.f);
+                            mma_f16(d, k[1][0], k[1][1], k[1][2], k[1][3], b0.z, b0.w);
+                            mma_f16(d, k[2][0], k[2][1], k[2][2], k[2][3], b1.x, b1.y);
+                            mma_f16(d, k[3][0], k[3][1], k[3][2], k[3][3], b1.z, b1.w);
+                            const float2 f0 = sb[z][g][0], f1 = sb[z][g][1];
+                            S4[0] = fmaf(f0.x, d[0], fmaf(f0.y, qs.x, S4[0]));
+                            S4[1] = fmaf(f0.x, d[1], fmaf(f0.y, qs.y, S4[1]));
+                            S4[2] = fmaf(f1.x, d[2], fmaf(f1.y, qs.x, S4[2]));
+                            S4[3] = fmaf(f1.x, d[3], fmaf(f1.y, qs.y, S4[3]));
                         }
                     }
-                    sum[z][0] += w[0] + w[1];
-                    sum[z][1] += w[2] + w[3];
+#pragma unroll
+                for (int y = 0; y < PAIR; y++) {
+                    const float2 lse = *reinterpret_cast<const float2*>(&s_lse[r0 + 8 * y + 2 * t4]);
+#pragma unroll
+                    for (int z = 0; z < SETS; z++) {
+                        const float(&S4)[4] = S[y][z];
+                        float w[4] = {exp2_fast(fmaf(S4[0], sl2, -lse.x)), exp2_fast(fmaf(S4[1], sl2, -lse.y)),
+                                      exp2_fast(fmaf(S4[2], sl2, -lse.x)), exp2_fast(fmaf(S4[3], sl2, -lse.y))};
+                        if (edge) {
+                            const int2 p = *reinterpret_cast<const int2*>(&s_pos[r0 + 8 * y + 2 * t4]);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const int j = j0 + 16 * z + 8 * (k >> 1) + g8, at = k & 1 ? p.y : p.x;
+                                if (j > at || (a.window > 0 && j <= at - a.window)) w[k] = 0.f;
+                            }
+                        }
+                        sum[z][0] += w[0] + w[1];
+                        sum[z][1] += w[2] + w[3];
+                    }
                 }
             }
         }
-        if (in && blk1 >= blk0) {
+        if (Sh::kSplit > 1) {                                            // the partner's sums, to the first of the two
+            if (warp >= Sh::kGroups) {
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    float v = sum[0][k];
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    if (t4 == 0) s_part[warp][8 * k + g8] = v;
+                }
+            }
+            __syncthreads();
+        }
+        if (in && blk1 >= blk0 && warp < Sh::kGroups) {
             float* score = c.score + ((size_t)s * c.hkv + h) * ((size_t)c.max_pages * kKvPage);
 #pragma unroll
             for (int z = 0; z < SETS; z++)
@@ -262,9 +293,11 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
                     v += __shfl_xor_sync(0xffffffffu, v, 1);
                     v += __shfl_xor_sync(0xffffffffu, v, 2);
                     const int j = j0 + 16 * z + 8 * k + g8;
+                    if (Sh::kSplit > 1) v += s_part[warp + Sh::kGroups][8 * k + g8];
                     if (t4 == 0 && j < q.len) score[j] += v;
                 }
         }
+        if (Sh::kSplit > 1) __syncthreads();                             // s_part is free again
     }
 }
 
