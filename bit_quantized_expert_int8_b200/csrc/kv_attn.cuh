@@ -143,13 +143,16 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // largest to 1024..2048, so that 16 q, for the even pairs, stays exact), keeps a running
 // maximum (moved only when it grows by more than 2^8, so the sums are rescaled
 // rarely) and adds
-//   O += sum_j p_j s_jg c_j,   B_g += sum_j p_j b_jg.
-// These products are taken transposed (rows = columns of V, columns = query
-// rows): the scores' registers are then the second operand as they stand, and 8
-// query rows fill a tile.  p s enters as two fp16 parts (hi, lo: 22 bits), kept
-// in fp16's range by a power of two per warp (unit) that is chosen at the first
-// entries and lowered when a later p s would leave the range; it is part of the
-// exponent that p is formed with.  The warps' sums
+//   O += sum_j p_j s_jg (c_j - 8),   B_g += sum_j p_j (b_jg + 8 s_jg).
+// Codes of V are centred: raw ones (0..15) would let O grow to many times the
+// result, and the tensor cores' accumulation, which cuts off, would cost 8e-4 of it
+// over 131,072 entries.  These products are taken transposed (rows = columns of V,
+// columns = query rows): the scores' registers are then the second operand as they
+// stand, and 8 query rows fill a tile.  p s enters as one fp16 value (a relative
+// 2^-12 per entry on average; a second one for the remainder made the kernel 8 %
+// slower), kept in fp16's range by a power of two per warp (unit) that is chosen at
+// the first entries and lowered when a later p s would leave the range; it is part
+// of the exponent that p is formed with.  The warps' sums
 // meet in shared memory; an item cut by CTA borders goes through partial sums in
 // the workspace, joined in a fixed order by the last CTA to arrive (one counter
 // per item start, reset by that CTA).
@@ -306,7 +309,7 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
     // the weighted sum, 16 entries at a time
 #pragma unroll
     for (int b = 0; b < 2; b++) {
-        uint32_t sb[NG][4], hi[NG][RT][2], lo[NG][RT][2];
+        uint32_t sb[NG][4], hi[NG][RT][2];
 #pragma unroll
         for (int g = 0; g < NG; g++) {
             const uint2 s0 = lds64(vb + 1024 * NG + g * 128 + b * 64 + t4 * 8);
@@ -328,8 +331,6 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
                         const float e0 = seen(z, 2 * k) ? p[z][4 * b + 2 * k] * f0.x : 0.f;
                         const float e1 = seen(z, 2 * k + 1) ? p[z][4 * b + 2 * k + 1] * f1.x : 0.f;
                         hi[g][z][k] = f2h(e0, e1);
-                        const float2 r = h2f(hi[g][z][k]);
-                        lo[g][z][k] = f2h(e0 - r.x, e1 - r.y);
                         big = __hmax2(big, __habs2(*reinterpret_cast<const __half2*>(&hi[g][z][k])));
                     }
             return fmaxf(__low2float(big), __high2float(big)) <= 32768.f;
@@ -372,25 +373,22 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const float2 f = h2f(sb[g][k]);
+                const float mid = fmaf(8.f, f.x, f.y);
 #pragma unroll
                 for (int z = 0; z < RT; z++)
-                    if (seen(z, k)) A.B[g][z] = fmaf(p[z][4 * b + k], f.y, A.B[g][z]);
+                    if (seen(z, k)) A.B[g][z] = fmaf(p[z][4 * b + k], mid, A.B[g][z]);
             }
             const uint32_t va = vb + g * 1024 + b * 512 + t4 * 32 + g8 * 4;
             const uint32_t w0 = lds32(va), w1 = lds32(va + 128), w2 = lds32(va + 256), w3 = lds32(va + 384);
-            uint32_t a0[4], a1[4], a2[4], a3[4];
-            code_pairs(__byte_perm(w0, w1, 0x5410), a0);
-            code_pairs(__byte_perm(w0, w1, 0x7632), a1);
-            code_pairs(__byte_perm(w2, w3, 0x5410), a2);
-            code_pairs(__byte_perm(w2, w3, 0x7632), a3);
+            const uint4 a0 = codes_centred(__byte_perm(w0, w1, 0x5410)), a1 = codes_centred(__byte_perm(w0, w1, 0x7632));
+            const uint4 a2 = codes_centred(__byte_perm(w2, w3, 0x5410)), a3 = codes_centred(__byte_perm(w2, w3, 0x7632));
 #pragma unroll
             for (int z = 0; z < RT; z++) {
-#pragma unroll
-                for (int jj = 0; jj < 4; jj++)
-                    mma_f16(A.O[z][g * 4 + jj], a0[jj], a1[jj], a2[jj], a3[jj], hi[g][z][0], hi[g][z][1]);
-#pragma unroll
-                for (int jj = 0; jj < 4; jj++)
-                    mma_f16(A.O[z][g * 4 + jj], a0[jj], a1[jj], a2[jj], a3[jj], lo[g][z][0], lo[g][z][1]);
+                float(*o)[4] = &A.O[z][g * 4];
+                mma_f16(o[0], a0.x, a1.x, a2.x, a3.x, hi[g][z][0], hi[g][z][1]);
+                mma_f16(o[1], a0.y, a1.y, a2.y, a3.y, hi[g][z][0], hi[g][z][1]);
+                mma_f16(o[2], a0.z, a1.z, a2.z, a3.z, hi[g][z][0], hi[g][z][1]);
+                mma_f16(o[3], a0.w, a1.w, a2.w, a3.w, hi[g][z][0], hi[g][z][1]);
             }
         }
     }
@@ -634,7 +632,6 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         cp_async_wait<0>();
 
         // join the warps: sums to shared memory (over the ring), relative to each warp's maximum
-        constexpr float inv = kCodeUnit, inv16 = kCodeUnit / 16.f;
 #pragma unroll
         for (int z = 0; z < RT; z++) {
             A.l[z] += __shfl_xor_sync(0xffffffffu, A.l[z], 1);
@@ -660,9 +657,9 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                     const float bb = row_value(A.B[g][z], k);
                     float4* dst = reinterpret_cast<float4*>(join + ((size_t)warp * R + 8 * z + 2 * t4 + k) * JR + g * 64 + g8 * 8);
                     const float(*v)[4] = &A.O[z][g * 4];
-                    dst[0] = make_float4(fmaf(v[0][k], inv, bb), fmaf(v[1][k], inv16, bb), fmaf(v[2][k], inv, bb), fmaf(v[3][k], inv16, bb));
-                    dst[1] = make_float4(fmaf(v[0][2 + k], inv, bb), fmaf(v[1][2 + k], inv16, bb), fmaf(v[2][2 + k], inv, bb),
-                                         fmaf(v[3][2 + k], inv16, bb));
+                    dst[0] = make_float4(v[0][k] + bb, v[1][k] + bb, v[2][k] + bb, v[3][k] + bb);
+                    dst[1] = make_float4(v[0][2 + k] + bb, v[1][2 + k] + bb, v[2][2 + k] + bb,
+                                         v[3][2 + k] + bb);
                 }
         __syncthreads();
         const bool whole = u == ie && ib >= blockIdx.x * per;

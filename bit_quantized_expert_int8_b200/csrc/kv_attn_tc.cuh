@@ -4,15 +4,16 @@
 // Rows of one kv head are its (row, query head) pairs; an item is (sequence,
 // tile of 128 rows, kv head).  Per page of 64 entries
 //   S[r][j] = q[r] . k[j]       tcgen05, Q and K in shared memory
-//   p = exp(S - max)            one row per pair of threads, fp16 P over S in tensor memory
+//   p = exp(S - max)            one row per pair of threads, P over S in tensor memory
 //   O[r][d] += P[r] . v[.][d]   tcgen05, P from tensor memory, V in shared memory
 // K enters as two fp16 operands, hi = fp16(s c + b) and lo = fp16(s c + b - hi),
 // so the scores are as exact as fp32 sums are.  (With the raw codes as operands
 // and the groups' scales folded in by the softmax threads, as the few-row kernel
 // does it, every thread reads every entry's scales from shared memory: 512
-// 16-byte broadcasts a tile, 5,000 cycles; this way a tile costs 1,500.)  V and p
-// are rounded to fp16 once, a relative 2^-12 each on average, below the rounding
-// of the output.  K and V are scaled by powers of two, so that no value leaves
+// 16-byte broadcasts a tile, 427 us against 334 at 4 chunks of 512.)  p enters as
+// hi and remainder too; V is rounded to fp16 once, a relative 2^-12 on average, as
+// the output is (one more rounding, of p, would make the error 1.7 times that of
+// the output's own rounding instead of 1.4).  K and V are scaled by powers of two, so that no value leaves
 // fp16's range: K's (per page) divides the softmax scale, V's (held until a page
 // exceeds it) leaves at the end.  The row maximum moves only when it grows by more
 // than 2^8, and only then is O rescaled.  Groups of V that are not finite enter as
@@ -422,10 +423,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     ls[(j >> 1) & 1] = add2(ls[(j >> 1) & 1], make_float2(S[j], S[j + 1]));
                 }
                 l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                uint32_t P[16];
+                uint32_t P[16];                          // hi, then the remainder behind it
 #pragma unroll
                 for (int j = 0; j < 16; j++) P[j] = f2h(S[2 * j], S[2 * j + 1]);
                 tmem_st16(t_s + half * (HK / 2), P);
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const float2 f = h2f(P[j]), d = add2(make_float2(S[2 * j], S[2 * j + 1]), make_float2(-f.x, -f.y));
+                    P[j] = f2h(d.x, d.y);
+                }
+                tmem_st16(t_s + KT / 2 + half * (HK / 2), P);
                 if (meta.any)
 #pragma unroll
                     for (int g = 0; g < NG; g++)
@@ -710,7 +717,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const uint32_t dv = (uint32_t)tc_sdesc_sw128(sV + (n % VR) * Sh::kV), pa = tmem + Sh::kS + st * KT;
                 tc_mma_ts(tmem + Sh::kO, pa, tc_desc(dv, dhi), id_o, t > 0 ? 1u : 0u);
 #pragma unroll
-                for (int k = 1; k < KT / 16; k++) tc_mma_ts_acc(tmem + Sh::kO, pa + 8 * k, tc_desc(dv + 2u * k, dhi), id_o);
+                for (int k = 1; k < KT / 8; k++)         // hi, then the remainder
+                    tc_mma_ts_acc(tmem + Sh::kO, pa + 8 * k, tc_desc(dv + 2u * (k % (KT / 16)), dhi), id_o);
                 mma_commit(&b_pv[n % VR]);
                 return true;
             };

@@ -46,6 +46,22 @@ def sequence(pages, table, n, Hkv, D):
     return kv[0], kv[1]
 
 
+def value_spread(pages, table, V, D):
+    """|V - (bias + 8 scale)| of a sequence's entries: the part scale * (code - 8)
+    of each value, in size."""
+    Hkv, n = V.shape[:2]
+    ng = D // 64
+    out = np.empty_like(V)
+    for p in range((n + PAGE - 1) // PAGE):
+        m = min(PAGE, n - p * PAGE)
+        f = np.ascontiguousarray(pages[table[p]][:, 4352 * ng:]).view(np.float16).astype(np.float64)
+        f = f.reshape(Hkv, ng, PAGE, 2)[:, :, :m]
+        with np.errstate(invalid="ignore"):
+            mid = np.repeat((f[..., 1] + 8 * f[..., 0]).transpose(0, 2, 1), 64, axis=2)
+            out[:, p * PAGE:p * PAGE + m] = np.abs(V[:, p * PAGE:p * PAGE + m] - mid)
+    return out
+
+
 def attention(q, K, V, scale, window, n_entries):
     """q [n][Hq][D] of a sequence with n_entries entries: out [n][Hq][D], lse
     [n][Hq] and the weight each entry received [Hkv][n_entries]."""

@@ -11,11 +11,12 @@ far end of its distribution.  The weighted sum adds 16-entry steps of at most
 beside the half step 2^-11 of its rounding to fp16 (2^-25 below the normal
 range).
 
-Sequences with more than 16 (row, head) pairs per kv head round twice more: the
-weight p to fp16 before it meets V, and V itself (scale * code + bias).  Each is off
-by at most half a step, 2^-11 of its size, so an output sum_j w_j v_j (w = p / sum p,
-the sum taken of the unrounded p) moves by at most 2 * 2^-11 sum_j w_j |v_j|, and by
-2^-22 of the same for both at once: the attention of |V|, which the reference forms.
+One more operand is rounded to fp16, off by at most half a step, 2^-11 of its size.
+With up to 16 (row, head) pairs per kv head it is p s, the weight times a group's
+scale: an output is sum_j p_j s_j (code_j - 8) + p_j (bias_j + 8 s_j) over sum p, so
+it moves by at most 2^-11 sum_j w_j |s_j (code_j - 8)| with w = p / sum p.  With more
+it is V itself, scale * code + bias: at most 2^-11 sum_j w_j |v_j|.  Both are
+attentions of absolute values, which the reference forms (spread).
 """
 import math
 
@@ -96,9 +97,13 @@ class Case:
                 continue
             K, V = kv_ref.sequence(self.pages, self.table[s], n, self.Hkv, self.D)
             out[a:b], lse[a:b], got[s, :, :n] = kv_ref.attention(q[a:b].astype(np.float64), K, V, scale, window, n)
-            if (b - a) * self.Hq // self.Hkv > 16:
-                spread[a:b] = kv_ref.attention(q[a:b].astype(np.float64), K, np.abs(V), scale, window, n)[0]
+            spread[a:b] = self.spread(s, q[a:b], K, V, scale, window, n)
         return out, lse, got, spread
+
+    def spread(self, s, q, K, V, scale, window, n):
+        few = q.shape[0] * self.Hq // self.Hkv <= 16
+        U = kv_ref.value_spread(self.pages, self.table[s], V, self.D) if few else np.abs(V)
+        return kv_ref.attention(q.astype(np.float64), K, U, scale, window, n)[0]
 
     def attend(self, q, scale, window=0, weights=False, **kw):
         out = torch.full((self.n_rows, self.Hq, self.D), 7.0, dtype=torch.float16, device=DEV)
@@ -113,7 +118,7 @@ def close(out, lse, ref, rows=None):
     ro, rl, rs = ref[0][:rows], ref[1][:rows], ref[3][:rows]
     out, lse = out[:rows], lse[:rows]
     assert np.isfinite(out).all()
-    off = np.abs(out - ro) - (2.0 ** -11 * np.abs(ro) + 2.001 * 2.0 ** -11 * rs + 2.0 ** -25 + 1e-4)
+    off = np.abs(out - ro) - (2.0 ** -11 * np.abs(ro) + 2.0 ** -11 * rs + 2.0 ** -25 + 1e-4)
     assert (off <= 0).all(), off.max()
     dead = np.isneginf(rl)
     assert (np.isneginf(lse) == dead).all()
@@ -208,7 +213,7 @@ def test_small_and_large_values(sigma):
     # q / sigma is rounded to fp16 (subnormal for 300) on both sides alike; the
     # code offset makes partial sums of the bias part about as large as above.
     # At 1e-4 the output itself is in fp16's subnormal range, where a half step is 2^-25
-    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + 2.001 * ref[3]) + 2.0 ** -25 + 1e-4 * sigma).all()
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 2.0 ** -25 + 1e-4 * sigma).all()
     assert (np.abs(lse - ref[1]) <= 1e-4).all()
 
 
@@ -229,7 +234,7 @@ def test_mixed_value_scales():
     q = c.queries()
     ref = c.reference(q, 0.05)
     out, lse = c.attend(q, 0.05)
-    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * np.abs(ref[0]) + 1e-4 * 100).all()
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 1e-4 * 100).all()
     # with the large pages masked away the small ones alone have to be exact
     c2 = Case(25, 128, 4, 1, [640], [1])
     for p in c2.table[0]:
@@ -239,7 +244,7 @@ def test_mixed_value_scales():
     c2.upload()
     ref = c2.reference(q, 0.05)
     out, lse = c2.attend(q, 0.05)
-    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * np.abs(ref[0]) + 2.0 ** -25 + 1e-4 * 2.0 ** -10).all()
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 2.0 ** -25 + 1e-4 * 2.0 ** -10).all()
 
 
 @pytest.mark.parametrize("rows,window", [([1, 1], 0), ([1, 1], 20), ([9, 40], 0), ([9, 40], 20), ([130, 140], 30)])
@@ -336,7 +341,9 @@ def test_pool_offsets_beyond_32_bits():
     moeq4.moe_attn_q4(kv, cache, batch, cu(q), out, lse=lse, scale=0.06)
     moeq4.moe_kv_check(kv)
     K, V = kv_ref.sequence(small, [0, 1, 2, 3], 250, Hkv, D)
-    ref = (*kv_ref.attention(q.astype(np.float64), K, V, 0.06, 0, 250), np.zeros((1, 8, D)))
+    U = kv_ref.value_spread(small, [0, 1, 2, 3], V, D)
+    ref = (*kv_ref.attention(q.astype(np.float64), K, V, 0.06, 0, 250),
+           kv_ref.attention(q.astype(np.float64), K, U, 0.06, 0, 250)[0])
     close(out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), ref)
     assert np.array_equal(pool[at[3] * per:(at[3] + 1) * per].cpu().numpy(), small[3].reshape(-1))
 
@@ -513,7 +520,7 @@ def test_bounded_decode_steps():
                 pos[s, :, at] = seen[s] - rows[s] + i
             K, V = kv_ref.sequence(pages, table[s], int(lens[s]), Hkv, D)
             ro, rl, w = kv_ref.attention(qkv[a:b, :Hq].astype(np.float64), K, V, 0.09, 0, int(lens[s]))
-            U = np.abs(V) if rows[s] * Hq // Hkv > 16 else 0 * V
+            U = np.abs(V) if rows[s] * Hq // Hkv > 16 else kv_ref.value_spread(pages, table[s], V, D)
             rs = kv_ref.attention(qkv[a:b, :Hq].astype(np.float64), K, U, 0.09, 0, int(lens[s]))[0]
             close(out[a:b].cpu().numpy().astype(np.float64), lse[a:b].cpu().numpy().astype(np.float64), (ro, rl, w, rs))
             score64[s, :, :lens[s]] += w
