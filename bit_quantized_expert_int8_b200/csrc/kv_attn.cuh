@@ -158,7 +158,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // per item start, reset by that CTA).
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitStages = 3;
+constexpr int kSplitStages = 2;        // 3 with 2 CTAs per SM: 100 us for 64 tokens, window 1024; 2 with 3: 84
 constexpr int kSplitMinUnits = 4;      // pages per CTA at least: fewer partial sums in small calls
 constexpr int kSplitItemCost = 4;
 constexpr int kSplitMaxRows = 16;      // (row, head) pairs per kv head: more go to the tile kernel
@@ -173,7 +173,7 @@ struct SplitShape {
     static constexpr int kJoin = kSplitWarps * kRows * kJoinRow * 4; // the warps' sums, over the ring
     static constexpr int kQ = NG * 4 * 32 * 16;                      // query operand, 16 rows (zeros behind 8)
     static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
-    static constexpr int kCtas = NG * RT <= 2 ? 3 : 2;               // per SM
+    static constexpr int kCtas = NG * RT <= 4 ? 3 : 2;               // per SM
 };
 
 struct SplitArgs {
