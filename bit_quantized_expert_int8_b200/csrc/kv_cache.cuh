@@ -215,10 +215,12 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
 // order-preserving 32-bit key (11 + 11 + 10 bits): every CTA counts its part,
 // the counts meet in the cluster's first CTA through distributed shared memory,
 // which finds the threshold.  A bit per entry then says whether it stays.  The r-th staying entry
-// behind the budget moves into the r-th free place below it; both are found by a
-// search in prefix counts over the words of bits, wherever in the cluster they
-// lie, so the ranks (and with them the copying) are shared evenly and no list
-// leaves shared memory.  The clusters are as large as fills the device (a cluster
+// behind the budget moves into the r-th free place below it.  Each CTA of the
+// cluster has an equal share of the ranks (and with them of the copying); the CTA
+// that holds an entry's bit writes the entry into the list of the CTA that has its
+// rank, by a store to distributed shared memory, which nobody waits for.  (Searching
+// the other CTAs' prefix counts instead took 21 of 63 us for half of 16384 entries.)
+// No list leaves shared memory.  The clusters are as large as fills the device (a cluster
 // per pair alone leaves most SMs idle when there are few pairs).
 constexpr int kEvictThreads = 512;
 constexpr int kEvictBins = 2048;
@@ -234,15 +236,15 @@ __device__ __forceinline__ uint32_t evict_key(float score, bool recent) {
 
 // Entries of one CTA at most, for a cluster of `parts`.
 __host__ __device__ constexpr int evict_part(int cap, int parts) { return ((cap + parts - 1) / parts + 31) / 32 * 32; }
-// bits, prefix counts, histogram, moves, and the keys of a part where they fit
+// Moves of one CTA that have room in its list at a time: all of a part of kEvictKeys / 2.
+__host__ __device__ constexpr int evict_room(int part) { return (part < kEvictKeys / 2 ? part : kEvictKeys / 2) / 2; }
+// histogram, the list of moves over the keys of a part (where these fit), bits, prefix counts
 __host__ __device__ constexpr size_t evict_smem(int part) {
-    return (size_t)(part / 32) * 4 + (size_t)(part / 32 + 2) * 4 + kEvictBins * 4 + kEvictThreads * 16 +
-           (part <= kEvictKeys ? (size_t)part * 4 : 0);
+    return kEvictBins * 4 + (size_t)evict_room(part) * 16 + (size_t)(part / 32) * 4 + (size_t)(part / 32 + 2) * 4;
 }
 
-// The most that a part of 524288 entries (max_pages 8192) asks for, alone or in a
-// cluster: without keys beyond kEvictKeys, with them up to there.
-constexpr int kEvictSmem = 148 * 1024;
+// The most that a part of 524288 entries (max_pages 8192) asks for, alone or in a cluster.
+constexpr int kEvictSmem = 204 * 1024;
 static_assert(evict_smem(524288) <= kEvictSmem && evict_smem(kEvictKeys) <= kEvictSmem, "eviction's shared memory");
 
 __device__ __forceinline__ int block_exclusive_scan(int v, int* s_scan, int* total) {
@@ -295,10 +297,10 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
     if (len <= budget) return;                                  // the whole cluster alike
     const int part_cap = evict_part(cap, C);
     uint32_t* hist = ev_smem;
-    int4* list = reinterpret_cast<int4*>(hist + kEvictBins);    // from, to, their pages
-    uint32_t* bits = reinterpret_cast<uint32_t*>(list + kEvictThreads);
+    uint32_t* keys = hist + kEvictBins;
+    int4* list = reinterpret_cast<int4*>(keys);                 // from and its page, to and its page; keys have been used
+    uint32_t* bits = keys + 4 * evict_room(part_cap);
     uint32_t* pre = bits + part_cap / 32;
-    uint32_t* keys = pre + part_cap / 32 + 2;
     const bool kept = part_cap <= kEvictKeys;
     const size_t at = ((size_t)s * a.hkv + h) * (size_t)cap;
     float* score = a.score + at;
@@ -406,26 +408,13 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
         s_mc[tid] = *cluster.map_shared_rank(&s_cnt[2], tid);
     }
     __syncthreads();
-    int moves = 0;
-    for (int r = 0; r < C; r++) moves += s_mc[r];
-    const int r0 = (int)((long long)moves * me / C), r1 = (int)((long long)moves * (me + 1) / C);
-    // the entry with rank k among free places (or entries to move) of the cluster
-    const auto find = [&](int k, const int* count, bool hole) {
-        int r = 0;
-        while (k >= count[r]) k -= count[r++];
-        const uint32_t* br = cluster.map_shared_rank(bits, r);
-        const uint32_t* pr = cluster.map_shared_rank(pre, r) + (hole ? 0 : 1);
-        const int b = r * part, nw = (min(len - b, part) + 31) / 32;
-        int lo = hole ? 0 : max(0, (budget - b) / 32), hi = (hole ? min(nw, (budget - b + 31) / 32) : nw) - 1;
-        while (lo < hi) {                                       // last word with prefix <= k
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int)pr[mid] <= k) lo = mid;
-            else hi = mid - 1;
-        }
-        uint32_t f = hole ? evict_holes(br[lo], b + lo * 32, budget) : evict_movers(br[lo], b + lo * 32, budget);
-        for (int q = k - (int)pr[lo]; q > 0; q--) f &= f - 1;
-        return b + lo * 32 + __ffs(f) - 1;
-    };
+    int moves = 0, hb = 0, mb = 0;                              // and the ranks before this part
+    for (int r = 0; r < C; r++) {
+        hb += r < me ? s_hc[r] : 0;
+        mb += r < me ? s_mc[r] : 0;
+        moves += s_mc[r];
+    }
+    const int share = (moves + C - 1) / C, room = evict_room(part_cap);
     const KvTile t(a.ng);
     // 2^sh lanes a move: 4 ng of them copy 16 bytes of codes, 2 ng a scale and bias, two the
     // score and the position; four moves a lane in flight
@@ -441,18 +430,29 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
     unit = (size_t)h * t.bytes() + off;
     const size_t page_bytes = (size_t)a.hkv * t.bytes();
     const int32_t* trow = a.table + (size_t)s * a.max_pages;
-    for (int k0 = r0; k0 < r1; k0 += kEvictThreads) {
-        const int m = min(kEvictThreads, r1 - k0);
-        if (tid < m) {
-            const int from = find(k0 + tid, s_mc, false), to = find(k0 + tid, s_hc, true);
-            int2 pg = make_int2(trow[from / kKvPage], trow[to / kKvPage]);
-            if ((unsigned)pg.x >= (unsigned)a.n_pages || (unsigned)pg.y >= (unsigned)a.n_pages) {
+    for (int k0 = 0; k0 < share; k0 += room) {
+        if (k0) cluster.sync();                                 // the lists have been worked through
+        // a lane per entry of a word tells the CTA that has its rank where it stands
+        for (int w = tid >> 5; w < words; w += kEvictThreads / 32) {
+            const int lo = e0 + w * 32;
+            const uint32_t holes = evict_holes(bits[w], lo, budget), movers = evict_movers(bits[w], lo, budget);
+            if (!(holes | movers)) continue;
+            int page = trow[lo / kKvPage];                      // a word lies in one page
+            if ((unsigned)page >= (unsigned)a.n_pages) {
                 kv_flag(a.status);
-                pg.x = -1;
+                page = -1;
             }
-            list[tid] = make_int4(from, to, pg.x, pg.y);
+            const auto tell = [&](uint32_t f, int before, int side) {
+                if (!(f >> lane & 1u)) return;
+                const int g = before + __popc(f & ((1u << lane) - 1u)), r = g / share, slot = g - r * share - k0;
+                if (g < moves && slot >= 0 && slot < room)
+                    reinterpret_cast<int2*>(cluster.map_shared_rank(list, r) + slot)[side] = make_int2(lo + lane, page);
+            };
+            if (movers) tell(movers, mb + (int)pre[w + 1], 0);
+            if (holes) tell(holes, hb + (int)pre[w], 1);
         }
-        __syncthreads();
+        cluster.sync();
+        const int m = min(room, min(share, moves - me * share) - k0);
         const int each = kEvictThreads >> sh;                   // moves in flight in a step
         for (int i0 = tid >> sh; i0 < m; i0 += 4 * each) {
             uint4 v[4];
@@ -461,9 +461,10 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
                 const int i = i0 + k * each;
                 if (i >= m) continue;
                 const int4 e = list[i];
-                const uint8_t* src = a.pages + (size_t)e.z * page_bytes + unit + (e.x % kKvPage) * step;
-                if (p < 4 * a.ng) { if (e.z >= 0) v[k] = *reinterpret_cast<const uint4*>(src); }
-                else if (p < 6 * a.ng) { if (e.z >= 0) v[k].x = *reinterpret_cast<const uint32_t*>(src); }
+                const bool ok = (e.y | e.w) >= 0;               // codes of a bad page stay where they are
+                const uint8_t* src = a.pages + (size_t)e.y * page_bytes + unit + (e.x % kKvPage) * step;
+                if (p < 4 * a.ng) { if (ok) v[k] = *reinterpret_cast<const uint4*>(src); }
+                else if (p < 6 * a.ng) { if (ok) v[k].x = *reinterpret_cast<const uint32_t*>(src); }
                 else if (p == 6 * a.ng) v[k].x = __float_as_uint(score[e.x]);
                 else if (p == 6 * a.ng + 1) v[k].x = (uint32_t)pos[e.x];
             }
@@ -472,16 +473,15 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
                 const int i = i0 + k * each;
                 if (i >= m) continue;
                 const int4 e = list[i];
-                uint8_t* dst = a.pages + (size_t)e.w * page_bytes + unit + (e.y % kKvPage) * step;
-                if (p < 4 * a.ng) { if (e.z >= 0) *reinterpret_cast<uint4*>(dst) = v[k]; }
-                else if (p < 6 * a.ng) { if (e.z >= 0) *reinterpret_cast<uint32_t*>(dst) = v[k].x; }
-                else if (p == 6 * a.ng) score[e.y] = __uint_as_float(v[k].x);
-                else if (p == 6 * a.ng + 1) pos[e.y] = (int)v[k].x;
+                const bool ok = (e.y | e.w) >= 0;
+                uint8_t* dst = a.pages + (size_t)e.w * page_bytes + unit + (e.z % kKvPage) * step;
+                if (p < 4 * a.ng) { if (ok) *reinterpret_cast<uint4*>(dst) = v[k]; }
+                else if (p < 6 * a.ng) { if (ok) *reinterpret_cast<uint32_t*>(dst) = v[k].x; }
+                else if (p == 6 * a.ng) score[e.z] = __uint_as_float(v[k].x);
+                else if (p == 6 * a.ng + 1) pos[e.z] = (int)v[k].x;
             }
         }
-        __syncthreads();
     }
-    cluster.sync();                                             // no CTA leaves while its bits are read
 }
 
 }  // namespace moeq4
