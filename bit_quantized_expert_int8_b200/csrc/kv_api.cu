@@ -70,7 +70,6 @@ struct moe_kv {
     MoeKvConfig cfg{};
     int device = 0;
     int n_sms = 0;
-    size_t smem_optin = 0;
     uint8_t* ws = nullptr;
     int* status = nullptr;     // [2]: what kernels report, a bounded wait that gave up
     float* lse = nullptr;      // [max_rows][n_q_heads], where the caller wants none
@@ -78,7 +77,6 @@ struct moe_kv {
     int* count = nullptr;      // arrivals per cut item, zero between calls
     int split_ctas[2] = {0, 0};  // CTAs of the split kernel: 8-row and 16-row tiles
     int split_smem[2] = {0, 0};
-    int tile_smem = 0;         // of the tile kernel; 0 where no call can have enough rows for it
     size_t counts = 0;         // length of count
     TileCut* cut = nullptr;    // [n_sms]
 };
@@ -165,6 +163,14 @@ extern "C" int moe_kv_destroy(moe_kv* kv) {
     return MOE_OK;
 }
 
+// Loads a kernel that nothing else here asks about, so that a context's first call
+// may be captured.
+template <typename F>
+static cudaError_t kv_load(F* fn) {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, fn);
+}
+
 extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     if (!out) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_create: out is NULL");
     *out = nullptr;
@@ -177,7 +183,6 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&kv->n_sms, cudaDevAttrMultiProcessorCount, kv->device);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, kv->device);
-    kv->smem_optin = (size_t)optin;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off = (off + bytes + 255) / 256 * 256; return o; };
     const size_t o_status = take(2 * sizeof(int));
@@ -205,8 +210,8 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     if (e == cudaSuccess && (int64_t)cfg->max_rows * (cfg->n_q_heads / cfg->n_kv_heads) > kSplitMaxRows) {
         const TileKernel k = tile_kernel(cfg->head_dim / 64);
         e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (e == cudaSuccess) e = kv_load(k.join);
         part = std::max(part, (size_t)2 * kv->n_sms * k.part_floats);
-        kv->tile_smem = k.smem;
     }
     const size_t o_part = take(part * sizeof(float));
     const size_t o_count = take(ctas * sizeof(int));
@@ -216,8 +221,16 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
         const WtKernel k = weights_kernel(cfg->head_dim / 64, many);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     }
+    if (e == cudaSuccess) e = kv_load(k_kv_rows<true, 1>);
+    if (e == cudaSuccess) e = kv_load(k_kv_rows<true, 8>);
+    if (e == cudaSuccess) e = kv_load(k_kv_rows<false, 1>);
+    if (e == cudaSuccess) e = kv_load(k_kv_rows<false, 8>);
     if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
-    if (e == cudaSuccess) e = cudaMemset(kv->ws, 0, off);
+    // what begins as zeros: the status, the arrival counts and the cut items
+    if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws + o_status, 0, 2 * sizeof(int), cudaStreamPerThread);
+    if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws + o_count, 0, ctas * sizeof(int), cudaStreamPerThread);
+    if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws + o_cut, 0, (size_t)kv->n_sms * sizeof(TileCut), cudaStreamPerThread);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamPerThread);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictSmem);
     if (e != cudaSuccess) {
         const int rc = kv_fail(MOE_ERR_CUDA, "moe_kv_create: %s", cudaGetErrorString(e));
@@ -233,26 +246,27 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     return MOE_OK;
 }
 
-extern "C" int moe_kv_check(moe_kv* kv, moe_stream_t stream) {
-    if (!kv) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_check: NULL context");
-    KV_CK(cudaStreamSynchronize(stream));
-    int st[2] = {0, 0};
-    KV_CK(cudaMemcpy(st, kv->status, sizeof(st), cudaMemcpyDeviceToHost));
-    if (st[0] == 0 && st[1] == 0) return MOE_OK;
-    KV_CK(cudaMemset(kv->status, 0, sizeof(st)));
-    if (st[1] != 0) {                  // some CTAs left early: the arrival counts begin anew
-        KV_CK(cudaMemset(kv->count, 0, kv->counts * sizeof(int)));
-        return kv_fail(st[1], "a bounded device wait of an attention call gave up; its outputs are not valid");
-    }
-    return kv_fail(st[0], "a KV cache kernel met a length, row start or page index outside its limits");
-}
-
 static int kv_check_device(const moe_kv* kv, const char* who) {
     int dev = -1;
     KV_CK(cudaGetDevice(&dev));
     if (dev != kv->device)
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: the context belongs to device %d, current is %d", who, kv->device, dev);
     return MOE_OK;
+}
+
+extern "C" int moe_kv_check(moe_kv* kv, moe_stream_t stream) {
+    if (!kv) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_check: NULL context");
+    KV_TRY(kv_check_device(kv, "moe_kv_check"));
+    int st[2] = {0, 0};
+    KV_CK(cudaMemcpyAsync(st, kv->status, sizeof(st), cudaMemcpyDeviceToHost, stream));
+    KV_CK(cudaStreamSynchronize(stream));
+    if (st[0] == 0 && st[1] == 0) return MOE_OK;
+    KV_CK(cudaMemsetAsync(kv->status, 0, sizeof(st), stream));
+    if (st[1] != 0) {                  // some CTAs left early: the arrival counts begin anew
+        KV_CK(cudaMemsetAsync(kv->count, 0, kv->counts * sizeof(int), stream));
+        return kv_fail(st[1], "a bounded device wait of an attention call gave up; its outputs are not valid");
+    }
+    return kv_fail(st[0], "a KV cache kernel met a length, row start or page index outside its limits");
 }
 
 static int kv_check_cache(const moe_kv* kv, const MoeKvCache* c, int n_seqs, const char* who) {
@@ -286,6 +300,17 @@ static int kv_check_rows(const void* p, int64_t stride, int heads, int D, const 
     return MOE_OK;
 }
 
+// Whether two row arrays share bytes: their spans meet, and they are not column
+// ranges of rows of one stride.
+static bool kv_overlap(const void* p, int64_t p_stride, int64_t p_width, const void* q, int64_t q_stride,
+                       int64_t q_width, int64_t rows) {
+    const int64_t a = (int64_t)(uintptr_t)p / 2, b = (int64_t)(uintptr_t)q / 2;
+    if (a + (rows - 1) * p_stride + p_width <= b || b + (rows - 1) * q_stride + q_width <= a) return false;
+    if (p_stride != q_stride) return true;
+    const int64_t d = ((b - a) % p_stride + p_stride) % p_stride;          // q's first column in p's rows
+    return d < p_width || d + q_width > p_stride;
+}
+
 static KvArgs kv_args(const moe_kv* kv, const MoeKvCache* c, const MoeKvBatch* b, int n_seqs) {
     KvArgs a{};
     a.pages = static_cast<uint8_t*>(c->pages);
@@ -317,6 +342,9 @@ static int kv_rows_call(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch* b
     KV_TRY(kv_check_batch(kv, batch, who));
     KV_TRY(kv_check_rows(k, k_stride, kv->cfg.n_kv_heads, kv->cfg.head_dim, who));
     KV_TRY(kv_check_rows(v, v_stride, kv->cfg.n_kv_heads, kv->cfg.head_dim, who));
+    const int64_t width = (int64_t)kv->cfg.n_kv_heads * kv->cfg.head_dim;
+    if (read && kv_overlap(k, k_stride, width, v, v_stride, width, batch->n_rows))
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: k and v overlap", who);
     KV_TRY(kv_check_device(kv, who));
     const KvArgs a = kv_args(kv, cache, batch, batch->n_seqs);
     __half* kp = reinterpret_cast<__half*>(k);
@@ -353,6 +381,9 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     KV_TRY(kv_check_batch(kv, batch, who));
     KV_TRY(kv_check_rows(q, q_stride, kv->cfg.n_q_heads, kv->cfg.head_dim, who));
     KV_TRY(kv_check_rows(out, out_stride, kv->cfg.n_q_heads, kv->cfg.head_dim, who));
+    const int64_t width = (int64_t)kv->cfg.n_q_heads * kv->cfg.head_dim;
+    if (kv_overlap(q, q_stride, width, out, out_stride, width, batch->n_rows))
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: q and out overlap", who);
     if (flags & ~MOE_ATTN_WEIGHTS) return kv_fail(MOE_ERR_INVALID_ARG, "%s: unknown flags 0x%x", who, flags);
     if (window < 0) return kv_fail(MOE_ERR_INVALID_ARG, "%s: window must be >= 0", who);
     if (!std::isfinite(scale)) return kv_fail(MOE_ERR_INVALID_ARG, "%s: scale must be finite", who);

@@ -96,7 +96,7 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
         return reinterpret_cast<uint4*>((is_v ? v + (size_t)r * v_stride : k + (size_t)r * k_stride) + (size_t)hg * 64) + w;
     };
     uint4 in[N];
-    if (!READ) {
+    if constexpr (!READ) {
 #pragma unroll
         for (int n = 0; n < N; n++) {
             in[n] = make_uint4(0, 0, 0, 0);
@@ -129,7 +129,7 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
         return make_ulonglong2((unsigned long long)(reinterpret_cast<uint32_t*>(tile + t.codes(part, g, en)) + w),
                                (unsigned long long)(tile + t.sb(part, g, en)));
     };
-    if (READ) {
+    if constexpr (READ) {
         uint32_t cw[N], sb[N];
 #pragma unroll
         for (int q = 0; q < N; q++) {
@@ -152,61 +152,61 @@ k_kv_rows(const KvArgs a, __half* k, long long k_stride, __half* v, long long v_
             }
             *row(it0 + 4 * q) = o;
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int q = 0; q < N; q++) {
-        const uint32_t iw[4] = {in[q].x, in[q].y, in[q].z, in[q].w};
-        float f[8];
-        bool fin = true;
+        for (int q = 0; q < N; q++) {
+            const uint32_t iw[4] = {in[q].x, in[q].y, in[q].z, in[q].w};
+            float f[8];
+            bool fin = true;
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&iw[c]));
-            f[2 * c] = p.x;
-            f[2 * c + 1] = p.y;
-            fin = fin && fabsf(p.x) <= 65504.f && fabsf(p.y) <= 65504.f;       // false for NaN
-        }
-        float lo = f[0], hi = f[0];
-#pragma unroll
-        for (int c = 1; c < 8; c++) {
-            lo = fminf(lo, f[c]);
-            hi = fmaxf(hi, f[c]);
-        }
-        int bad = fin ? 0 : 1;
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-        }
-        if (it0 + 4 * q >= items) continue;
-        const __half sc = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
-        const __half bi = __float2half_rn(lo);
-        const float sf = __half2float(sc), bf = __half2float(bi);
-        uint32_t c = 0;
-        if (!bad && sf != 0.f) {
-            // the correctly rounded quotient from the correctly rounded reciprocal and one
-            // corrected step (P. Markstein, IBM J. Res. Dev. 34 (1990), theorem on division)
-            const float rs = __frcp_rn(sf);
-#pragma unroll
-            for (int x = 0; x < 8; x++) {
-                const float d = f[x] - bf, q0 = d * rs;
-                const float u = rintf(fmaf(fmaf(-q0, sf, d), rs, q0));
-                c |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * x);
+            for (int c = 0; c < 4; c++) {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&iw[c]));
+                f[2 * c] = p.x;
+                f[2 * c + 1] = p.y;
+                fin = fin && fabsf(p.x) <= 65504.f && fabsf(p.y) <= 65504.f;       // false for NaN
             }
+            float lo = f[0], hi = f[0];
+#pragma unroll
+            for (int c = 1; c < 8; c++) {
+                lo = fminf(lo, f[c]);
+                hi = fmaxf(hi, f[c]);
+            }
+            int bad = fin ? 0 : 1;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            }
+            if (it0 + 4 * q >= items) continue;
+            const __half sc = __float2half_rn(__fdiv_rn(hi - lo, 15.0f));
+            const __half bi = __float2half_rn(lo);
+            const float sf = __half2float(sc), bf = __half2float(bi);
+            uint32_t c = 0;
+            if (!bad && sf != 0.f) {
+                // the correctly rounded quotient from the correctly rounded reciprocal and one
+                // corrected step (P. Markstein, IBM J. Res. Dev. 34 (1990), theorem on division)
+                const float rs = __frcp_rn(sf);
+#pragma unroll
+                for (int x = 0; x < 8; x++) {
+                    const float d = f[x] - bf, q0 = d * rs;
+                    const float u = rintf(fmaf(fmaf(-q0, sf, d), rs, q0));
+                    c |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * x);
+                }
+            }
+            const ulonglong2 at = codes(it0 + 4 * q);
+            *reinterpret_cast<uint32_t*>(at.x) = c;
+            if (w == 0)
+                *reinterpret_cast<__half2*>(at.y) = bad ? __halves2half2(__ushort_as_half(0x7FFF), __ushort_as_half(0x7FFF))
+                                                        : __halves2half2(sc, bi);
         }
-        const ulonglong2 at = codes(it0 + 4 * q);
-        *reinterpret_cast<uint32_t*>(at.x) = c;
-        if (w == 0)
-            *reinterpret_cast<__half2*>(at.y) = bad ? __halves2half2(__ushort_as_half(0x7FFF), __ushort_as_half(0x7FFF))
-                                                    : __halves2half2(sc, bi);
+        if (job % chunks == 0)
+            for (int h = lane; h < a.hkv; h += 32) {
+                const size_t at = ((size_t)s * a.hkv + h) * ((size_t)a.max_pages * kKvPage) + e;
+                if (a.score) a.score[at] = 0.f;
+                if (a.pos) a.pos[at] = a.seen[s] - n + i;
+            }
     }
-    if (job % chunks == 0)
-        for (int h = lane; h < a.hkv; h += 32) {
-            const size_t at = ((size_t)s * a.hkv + h) * ((size_t)a.max_pages * kKvPage) + e;
-            if (a.score) a.score[at] = 0.f;
-            if (a.pos) a.pos[at] = a.seen[s] - n + i;
-        }
 }
 
 // -------------------------------------------------------------- eviction --

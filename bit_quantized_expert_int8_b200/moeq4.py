@@ -422,6 +422,7 @@ class Kv:
         h = ctypes.c_void_p()
         _check(load().moe_kv_create(ctypes.byref(c), ctypes.byref(h)))
         self.handle = h.value
+        self.device = torch.cuda.current_device()
 
     def close(self):
         if self.handle:
@@ -435,8 +436,10 @@ class Kv:
             pass
 
 
-def _need(t, name, dtype, min_numel):
-    """A contiguous tensor of the given type that holds at least min_numel."""
+def _need(kv, t, name, dtype, min_numel):
+    """A contiguous tensor of the given type on the context's device that holds at least min_numel."""
+    if t.get_device() != kv.device:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} is not on the context's device")
     if t.dtype is not dtype or not t.is_contiguous() or t.numel() < min_numel:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} with at least {min_numel} elements")
 
@@ -450,17 +453,20 @@ class KvCache:
     def __init__(self, kv: Kv, pages, page_table, lens, score=None, pos=None, seen=None):
         c = kv.cfg
         n = lens.numel()
+        if pages.get_device() != kv.device:
+            raise MoeError(MOE_ERR_INVALID_ARG, "pages are not on the context's device")
         if not pages.is_contiguous() or \
                 pages.numel() * pages.element_size() < c.n_pages * kv_page_bytes(c.n_kv_heads, c.head_dim):
             raise MoeError(MOE_ERR_INVALID_ARG, "pages must be contiguous and hold n_pages pages")
-        _need(lens, "lens", torch.int32, 0)
-        _need(page_table, "page_table", torch.int32, n * c.max_pages)
+        _need(kv, lens, "lens", torch.int32, 0)
+        _need(kv, page_table, "page_table", torch.int32, n * c.max_pages)
         per = n * c.n_kv_heads * c.max_pages * MOE_KV_PAGE
         for t, name, dt, k in ((score, "score", torch.float32, per), (pos, "pos", torch.int32, per),
                                (seen, "seen", torch.int32, n)):
             if t is not None:
-                _need(t, name, dt, k)
+                _need(kv, t, name, dt, k)
         self.n_seqs = n
+        self.cfg, self.device = c, kv.device
         self.keep = (pages, page_table, lens, score, pos, seen)
         self.c = CMoeKvCache(*[_ptr(t) for t in self.keep])
         self.ref = ctypes.addressof(self.c)
@@ -471,16 +477,19 @@ class KvBatch:
     (device), the rows of the row arrays and the most rows of one sequence."""
 
     def __init__(self, kv: Kv, row_start, n_rows: int, max_q: int):
-        _need(row_start, "row_start", torch.int32, 1)
+        _need(kv, row_start, "row_start", torch.int32, 1)
         self.n_seqs = row_start.numel() - 1
         self.n_rows = int(n_rows)
+        self.device = kv.device
         self.keep = row_start
         self.c = CMoeKvBatch(self.n_seqs, self.n_rows, int(max_q), 0, row_start.data_ptr())
         self.ref = ctypes.addressof(self.c)
 
 
-def _rows(t, name, n_rows, heads, dim):
+def _rows(kv, t, name, n_rows, heads, dim):
     """Row stride of an fp16 [n_rows][heads][dim] tensor whose heads are contiguous."""
+    if t.get_device() != kv.device:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} is not on the context's device")
     if t.dtype is torch.float16 and t.dim() == 3:
         n, h, d = t.shape
         s0, s1, s2 = t.stride()
@@ -495,7 +504,12 @@ def _kv_stream(s):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if s is None else _stream(s)
 
 
-def _seqs(cache, n_seqs):
+def _fits(kv, cache, n_seqs, batch=None):
+    """A cache (and batch) made for this context's shape and device."""
+    if cache.cfg is not kv.cfg and cache.cfg != kv.cfg:
+        raise MoeError(MOE_ERR_INVALID_ARG, "the cache was made for a context of another shape")
+    if cache.device != kv.device or (batch is not None and batch.device != kv.device):
+        raise MoeError(MOE_ERR_INVALID_ARG, "the cache or batch was made for a context of another device")
     if n_seqs > cache.n_seqs:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{n_seqs} sequences in a cache of {cache.n_seqs}")
 
@@ -509,11 +523,10 @@ def moe_kv_check(kv, stream=None):
 def _kv_rows_call(fn, kv, cache, batch, k, v, stream):
     c = kv.cfg
     n = batch.n_rows
-    if batch.n_seqs > cache.n_seqs:
-        _seqs(cache, batch.n_seqs)
+    _fits(kv, cache, batch.n_seqs, batch)
     rc = fn(kv.handle, cache.ref, batch.ref,
-            k.data_ptr(), _rows(k, "k", n, c.n_kv_heads, c.head_dim),
-            v.data_ptr(), _rows(v, "v", n, c.n_kv_heads, c.head_dim), _kv_stream(stream))
+            k.data_ptr(), _rows(kv, k, "k", n, c.n_kv_heads, c.head_dim),
+            v.data_ptr(), _rows(kv, v, "v", n, c.n_kv_heads, c.head_dim), _kv_stream(stream))
     if rc:
         _check(rc)
 
@@ -532,22 +545,21 @@ def moe_attn_q4(kv, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=1.0,
     entry received to the cache's scores (MOE_ATTN_WEIGHTS)."""
     c = kv.cfg
     n, heads, dim = batch.n_rows, c.n_q_heads, c.head_dim
-    if batch.n_seqs > cache.n_seqs:
-        _seqs(cache, batch.n_seqs)
+    _fits(kv, cache, batch.n_seqs, batch)
     if lse is not None:
-        _need(lse, "lse", torch.float32, n * heads)
+        _need(kv, lse, "lse", torch.float32, n * heads)
     rc = load().moe_attn_q4(kv.handle, cache.ref, batch.ref,
-                            q.data_ptr(), _rows(q, "q", n, heads, dim), scale, window,
+                            q.data_ptr(), _rows(kv, q, "q", n, heads, dim), scale, window,
                             MOE_ATTN_WEIGHTS if weights else 0,
-                            out.data_ptr(), _rows(out, "out", n, heads, dim),
+                            out.data_ptr(), _rows(kv, out, "out", n, heads, dim),
                             None if lse is None else lse.data_ptr(), _kv_stream(stream))
     if rc:
         _check(rc)
 
 
 def moe_kv_evict(kv, cache: KvCache, n_seqs, budget, n_recent, new_lens, stream=None):
-    _seqs(cache, n_seqs)
-    _need(new_lens, "new_lens", torch.int32, n_seqs)
+    _fits(kv, cache, n_seqs)
+    _need(kv, new_lens, "new_lens", torch.int32, n_seqs)
     rc = load().moe_kv_evict(kv.handle, cache.ref, n_seqs, budget, n_recent, new_lens.data_ptr(),
                              _kv_stream(stream))
     if rc:

@@ -576,7 +576,8 @@ int moe_kv_create(const MoeKvConfig *cfg, moe_kv **out);
 int moe_kv_destroy(moe_kv *kv);
 
 /* Synchronises `stream`; MOE_ERR_INVALID_ARG if a kernel of this context met
- * a length, row start or page index outside its limits since the last check. */
+ * a length, row start or page index outside its limits since the last check,
+ * MOE_ERR_TIMEOUT if a bounded wait inside an attention call gave up. */
 int moe_kv_check(moe_kv *kv, moe_stream_t stream);
 
 /* Quantises the call's new rows into their entries: per row, kv head and
@@ -593,7 +594,8 @@ int moe_kv_append_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batc
                      moe_stream_t stream);
 
 /* The inverse: the entries of the call's rows as fp16(scale * code + bias)
- * (formed in fp32).  Same arguments as the append that wrote them. */
+ * (formed in fp32).  Same arguments as the append that wrote them; k and v must
+ * not overlap. */
 int moe_kv_read_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch,
                    moe_half *k, int64_t k_stride, moe_half *v, int64_t v_stride,
                    moe_stream_t stream);
@@ -606,7 +608,8 @@ int moe_kv_read_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch,
  * A row that sees nothing (lens[s] < n) gets out = 0 and lse = -infinity.
  * Entries outside a row's range never touch its result, whatever their pages
  * hold.
- *   q    device fp16 [n_rows][n_q_heads][head_dim], out likewise
+ *   q    device fp16 [n_rows][n_q_heads][head_dim], out likewise; they must not
+ *        overlap (both may be columns of the same rows)
  *   lse  device fp32 [n_rows][n_q_heads] or NULL
  * flags & MOE_ATTN_WEIGHTS: also adds to cache->score, for every entry j and
  * kv head, sum exp(S_j - lse) over the sequence's rows and the kv head's query

@@ -135,7 +135,7 @@ SHAPES = [
     (192, 10, 2, [333, 511], [1, 2], 0),
     (256, 16, 2, [500, 77], [1, 1], 0),
     (256, 5, 1, [260, 1500], [1, 1], 100),
-    (128, 24, 2, [400, 90], [1, 1], 0),                # 12 heads a kv head
+    (128, 22, 2, [400, 90], [1, 1], 0),                # 11 heads a kv head
     (128, 20, 1, [200], [1], 0),                       # 20 heads a kv head
     (128, 8, 2, [700, 70, 300], [3, 4, 2], 0),         # a few rows each
     (64, 4, 2, [100, 0, 50], [0, 0, 5], 0),            # sequences without rows or entries
@@ -356,17 +356,17 @@ def test_append_and_read(D, Hkv, lens, rows):
     c = Case(41 + D, D, Hkv, Hkv, lens, rows, spare_rows=2, state=True)
     c.seen += 1000
     c.upload()
-    qkv = c.rng.standard_normal((c.n_rows, 3 * Hkv, D)).astype(np.float16)
+    qkv = c.rng.standard_normal((c.n_rows, 3 * Hkv + 1, D)).astype(np.float16)
     qkv[0, 0, :64] = 1.5                               # a constant group
     qkv[0, Hkv, :] = 0
     if c.n_rows > 3:
         qkv[1, 0, 5] = np.inf
         qkv[1, -1, 7] = np.nan
         qkv[2, 1 % Hkv] *= np.float16(6e-6)            # subnormal scales
-        qkv[2, 2 * Hkv] = np.where(np.arange(D) % 2, 65504, -65504)
-    k, v = qkv[:, :Hkv], qkv[:, 2 * Hkv:]
+        qkv[2, 2 * Hkv + 1] = np.where(np.arange(D) % 2, 65504, -65504)
+    k, v = qkv[:, :Hkv], qkv[:, 2 * Hkv + 1:]
     g = cu(qkv)
-    moeq4.moe_kv_append_q4(c.kv, c.cache, c.batch, g[:, :Hkv], g[:, 2 * Hkv:])
+    moeq4.moe_kv_append_q4(c.kv, c.cache, c.batch, g[:, :Hkv], g[:, 2 * Hkv + 1:])
     ko = torch.full((c.n_rows, Hkv, D), 7.0, dtype=torch.float16, device=DEV)
     vo = torch.full((c.n_rows, Hkv + 1, D), 7.0, dtype=torch.float16, device=DEV)
     moeq4.moe_kv_read_q4(c.kv, c.cache, c.batch, ko, vo[:, :Hkv])
@@ -589,6 +589,94 @@ def test_another_stream():
     close(out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), c.reference(q, 0.09))
 
 
+@pytest.mark.parametrize("seed", range(3))
+def test_many_ragged_sequences(seed):
+    """Sequences of few and of many rows in one call, and a larger max_q than any has."""
+    rng = np.random.default_rng(100 + seed)
+    n = [45, 70, 33][seed]
+    rows = [int(x) for x in rng.choice([0, 1, 2, 5, 17, 40, 150], n)]
+    lens = [int(r + x) for r, x in zip(rows, rng.integers(0, 400, n))]
+    D, Hq, Hkv = [(64, 6, 2), (128, 4, 2), (192, 3, 1)][seed]
+    c = Case(66 + seed, D, Hq, Hkv, lens, rows, spare_rows=7, state=True)
+    q = c.queries()
+    ref = c.reference(q, 0.1, 90)
+    c.batch = moeq4.KvBatch(c.kv, c.g["start"], c.n_rows, c.n_rows)
+    out, lse = c.attend(q, 0.1, 90, weights=True)
+    close(out, lse, ref, int(c.start[-1]))
+    want = c.score.astype(np.float64) + ref[2]
+    got = c.g["score"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= 1e-4 * ref[2] + 2.0 ** -23 * np.abs(want) + 1e-6).all()
+
+
+def test_two_contexts_on_two_streams():
+    """Calls of two contexts at once give what each gives alone."""
+    cs = [Case(67, 128, 8, 2, [3000, 700], [1, 60], state=True), Case(68, 128, 16, 4, [900, 2000], [150, 1], state=True)]
+    qs = [cu(c.queries()) for c in cs]
+    alone, outs, scores = [], [], []
+    for c, q in zip(cs, qs):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        moeq4.moe_attn_q4(c.kv, c.cache, c.batch, q, out, lse=lse, scale=0.09, weights=True)
+        alone.append((out, lse, c.g["score"].clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(8):
+        for c, q, st in zip(cs, qs, streams):
+            with torch.cuda.stream(st):
+                c.g["score"].copy_(cu(c.score))
+                out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+                moeq4.moe_attn_q4(c.kv, c.cache, c.batch, q, out, lse=lse, scale=0.09, weights=True)
+                outs.append((out, lse))
+                scores.append(c.g["score"].clone())
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(outs):
+        want = alone[i % 2]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(scores[i], want[2])
+
+
+def test_first_call_captured():
+    """A fresh context's first calls are captured, with many rows and an eviction, and
+    replayed on new contents."""
+    c = Case(69, 128, 8, 2, [700, 400], [100, 60], state=True)
+    e = Case(69, 128, 8, 2, [700, 400], [100, 60], state=True)      # the same, for eager calls
+    k, v = torch.randn((2, 160, 2, 128), dtype=torch.float16, device=DEV)
+    q = cu(c.queries())
+
+    def step(x, out, lse, new):
+        moeq4.moe_kv_append_q4(x.kv, x.cache, x.batch, k, v)
+        moeq4.moe_attn_q4(x.kv, x.cache, x.batch, q, out, lse=lse, scale=0.09, weights=True)
+        moeq4.moe_kv_evict(x.kv, x.cache, 2, 350, 20, new)
+
+    def outputs():
+        return torch.zeros_like(q), torch.zeros((160, 8), device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+
+    got, want = outputs(), outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c, *got)
+    for rep in range(3):
+        k.mul_(-1.5)
+        q.neg_()
+        graph.replay()
+        step(e, *want)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        for name in ("pages", "score", "pos"):
+            assert torch.equal(c.g[name].view(torch.uint8), e.g[name].view(torch.uint8)), name
+    moeq4.moe_kv_check(c.kv)
+
+
+def test_queries_and_outputs_in_the_same_rows():
+    c = Case(70, 128, 8, 2, [300, 90], [1, 40])
+    q = c.queries()
+    both = torch.full((41, 16, 128), 7.0, dtype=torch.float16, device=DEV)
+    both[:, 8:] = cu(q)
+    lse = torch.empty((41, 8), device=DEV)
+    moeq4.moe_attn_q4(c.kv, c.cache, c.batch, both[:, 8:], both[:, :8], lse=lse, scale=0.09)
+    close(both[:, :8].cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), c.reference(q, 0.09))
+    assert np.array_equal(both[:, 8:].cpu().numpy(), q)
+
+
 def test_nothing_to_do():
     c = Case(64, 64, 2, 1, [10], [1])
     q = torch.zeros((0, 2, 64), dtype=torch.float16, device=DEV)
@@ -634,6 +722,17 @@ def test_refusals():
     refused(shp, att, c.kv, c.cache, moeq4.KvBatch(c.kv, c.g["start"], 4, 2),
             torch.zeros((4, 8, 128), dtype=torch.float16, device=DEV), torch.zeros((4, 8, 128), dtype=torch.float16, device=DEV))
     refused(inv, att, c.kv, c.cache, moeq4.KvBatch(c.kv, c.g["start"], 3, 0), q, out)
+    refused(inv, att, c.kv, c.cache, c.batch, q, q)                             # in place
+    flat = torch.zeros((3, 12, 128), dtype=torch.float16, device=DEV)
+    refused(inv, att, c.kv, c.cache, c.batch, flat[:, :8], flat[:, 4:])         # columns that overlap
+    refused(inv, moeq4.moe_kv_read_q4, c.kv, c.cache, c.batch, k, k)
+    refused(inv, att, c.kv, c.cache, c.batch, q.cpu(), out)
+    refused(inv, att, c.kv, c.cache, c.batch, q, out.cpu())
+    refused(inv, moeq4.moe_kv_append_q4, c.kv, c.cache, c.batch, k, k.cpu())
+    refused(inv, moeq4.KvBatch, c.kv, c.g["start"].cpu(), 3, 2)
+    refused(inv, moeq4.KvCache, c.kv, c.g["pages"].cpu(), c.g["table"], c.g["lens"])
+    other = Case(71, 128, 8, 2, [100, 50], [1, 2], max_pages=9)
+    refused(inv, att, c.kv, other.cache, c.batch, q, out)                       # pages of another layout
     bare = moeq4.KvCache(c.kv, c.g["pages"], c.g["table"], c.g["lens"])
     refused(inv, att, c.kv, bare, c.batch, q, out, weights=True)
     refused(inv, moeq4.KvCache, c.kv, c.g["pages"][1:], c.g["table"], c.g["lens"])

@@ -1,9 +1,11 @@
 """4-bit KV cache, host side: sizes, refusals that need no GPU, and pins of the
 64-bit reference that the GPU tests compare with."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
+import torch
 
 import kv_ref
 from bit_quantized_expert_int8_b200 import build, moeq4
@@ -55,6 +57,18 @@ def test_null_arguments_are_refused():
     assert lib.moe_kv_read_q4(None, None, None, None, 0, None, 0, None) == moeq4.MOE_ERR_INVALID_ARG
     assert lib.moe_attn_q4(None, None, None, None, 0, 1.0, 0, 0, None, 0, None, None) == moeq4.MOE_ERR_INVALID_ARG
     assert lib.moe_kv_evict(None, None, 1, 1, 0, None, None) == moeq4.MOE_ERR_INVALID_ARG
+
+
+def test_host_tensors_are_refused():
+    kv = types.SimpleNamespace(cfg=KvConfig(**GOOD), device=0, handle=None)
+    i32 = dict(dtype=torch.int32)
+    pages = torch.zeros(4 * moeq4.kv_page_bytes(2, 128), dtype=torch.uint8)
+    for f in (lambda: moeq4.KvCache(kv, pages, torch.zeros((2, 2), **i32), torch.zeros(2, **i32)),
+              lambda: moeq4.KvBatch(kv, torch.zeros(3, **i32), 2, 1),
+              lambda: moeq4._rows(kv, torch.zeros((2, 8, 128), dtype=torch.float16), "q", 2, 8, 128)):
+        with pytest.raises(moeq4.MoeError) as ei:
+            f()
+        assert ei.value.code == moeq4.MOE_ERR_INVALID_ARG and "device" in str(ei.value)
 
 
 def test_reference_reads_what_it_appends():
