@@ -108,11 +108,11 @@ static TileKernel tile_kernel(int ng) {
 typedef void (*WtFn)(const AttnArgs);
 struct WtKernel {
     WtFn fn;
-    int smem;
+    int smem, ctas;
 };
 template <int NG, bool MANY>
 static WtKernel weights_of() {
-    return {k_attn_weights<NG, MANY>, WtShape<NG, MANY>::kSmem};
+    return {k_attn_weights<NG, MANY>, WtShape<NG, MANY>::kSmem, WtShape<NG, MANY>::kCtas};
 }
 static WtKernel weights_kernel(int ng, bool many) {
     static const WtKernel table[4][2] = {{weights_of<1, false>(), weights_of<1, true>()},
@@ -418,7 +418,7 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     }
     if (flags & MOE_ATTN_WEIGHTS) {
         const WtKernel k = weights_kernel(a.c.ng, most > kWtBlock);
-        KV_CK(kv_launch(1, k.fn, dim3(2 * kv->n_sms), kWtThreads, k.smem, stream, a));
+        KV_CK(kv_launch(1, k.fn, dim3(k.ctas * kv->n_sms), kWtThreads, k.smem, stream, a));
     }
     return MOE_OK;
 }

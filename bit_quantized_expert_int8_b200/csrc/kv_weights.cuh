@@ -9,14 +9,21 @@
 // over all query rows, which come in blocks of 64 through shared memory; each
 // thread sums its entries' weights over rows in a register, and every score is
 // written by one thread: the result does not depend on the order in which CTAs
-// run.  With few rows the kernel is bound by reading K, with many by the fold of
-// the groups' sums (S = sum_g s_g q_g . (c_g - 8) + (b_g + 8 s_g) sum(q_g)) and the
-// exponentials.  A unit is what the eight warps of a CTA hold at once: 256 entries
-// (128 with wide heads) when rows are few; 64 when there are many (MANY), each 16
-// held by two warps that take every second 8 rows and add up at the end, because
-// the entries alone do not fill the device (256 rows over 2,900 entries: 96 units of
-// 256, 127 us; 368 of 64).  CTAs take equal runs of units, over all sequences and kv
-// heads.
+// run.  Scores are S = sum_g s_g q_g . (c_g - 8) + (b_g + 8 s_g) sum(q_g).
+//
+// A unit is what the eight warps of a CTA hold at once.  Few rows (one block, up to
+// kWtBlock (row, head) pairs): 256 entries, 128 with wide heads; the queries stay in
+// shared memory while sequence and kv head do, and reading K is the bound.  More
+// (MANY): 64 entries, each 16 held by two warps that take every second pair of row
+// tiles and add up at the end, because the entries alone do not fill the device (256
+// rows of 5 heads over 2,900 entries: 96 units of 256, 127 us; 368 of 64).  Blocks of
+// rows then come by asynchronous copies, two blocks ahead, and ldmatrix deals them to
+// the threads as they lie, with the codes of K dealt to match: bringing every block
+// into operand order in registers, for every unit, was 40 % of the instructions (the
+// whole call 150 us, now 132, of which 50 are this kernel).  What bounds it there is
+// issue (51 % of the slots; 28 % of the tensor pipe, 14 % of the exponentials'), with
+// three CTAs per SM; two take 153 us.  CTAs take equal runs of units, over all
+// sequences and kv heads.
 #pragma once
 #include "kv_attn.cuh"
 
@@ -25,6 +32,18 @@ namespace moeq4 {
 constexpr int kWtWarps = 8;
 constexpr int kWtThreads = kWtWarps * 32;
 constexpr int kWtBlock = 64;           // query rows in shared memory
+constexpr uint32_t kOnes = 0x3C003C00u; // fp16 1, 1
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {     // else zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(at) : "memory");
+}
 
 template <int NG, bool MANY>
 struct WtShape {
@@ -34,7 +53,10 @@ struct WtShape {
     static constexpr int kSplit = kWtWarps / kGroups;           // warps that share the rows of the same entries
     static constexpr int kUnit = kGroups * 16 * kSets;          // entries a CTA holds: 4, 2 or 1 pages
     static constexpr int kQ = NG * 2 * 32 * 16;                 // operands of 8 query rows, bytes
-    static constexpr int kSmem = kWtBlock / 8 * kQ;
+    static constexpr int kBufs = MANY ? 3 : 1;                  // blocks of query rows in shared memory
+    static constexpr int kBlock = kWtBlock / 8 * kQ;
+    static constexpr int kSmem = kBufs * kBlock;
+    static constexpr int kCtas = MANY && NG <= 2 ? 3 : 2;       // per SM
 };
 
 struct WtSeq {
@@ -54,13 +76,13 @@ __device__ __forceinline__ WtSeq wt_seq(const AttnArgs& a, int s) {
 }
 
 template <int NG, bool MANY>
-__global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a) {
+__global__ void __launch_bounds__(kWtThreads, WtShape<NG, MANY>::kCtas) k_attn_weights(const AttnArgs a) {
     using Sh = WtShape<NG, MANY>;
     constexpr int D = Sh::kD, SETS = Sh::kSets, UNIT = Sh::kUnit;
     extern __shared__ __align__(128) uint8_t wt_smem[];
-    __shared__ __align__(16) float s_qs[kWtBlock / 8][NG][8];
-    __shared__ __align__(16) float s_lse[kWtBlock];
-    __shared__ __align__(16) int s_pos[kWtBlock];
+    __shared__ __align__(16) float s_qs[Sh::kBufs][kWtBlock / 8][NG][8];
+    __shared__ __align__(16) float s_lse[Sh::kBufs][kWtBlock];
+    __shared__ __align__(16) int s_pos[Sh::kBufs][kWtBlock];
     __shared__ float s_part[kWtWarps][16];
     __shared__ long long s_total, s_base0;
     __shared__ int s_seq;
@@ -105,9 +127,11 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
     long long u = blockIdx.x * per, base = s_base0;
     const long long u_end = min(total, u + per);
     if (u >= u_end) return;
-    int s = s_seq, h_now = -1, s_now = -1, blk_now = -1;
+    int s = s_seq, h_now = -1, s_now = -1;
     WtSeq q = wt_seq<UNIT>(a, s);
-    const uint32_t qb = smem_u32(wt_smem);
+    const uint32_t sb_q = smem_u32(wt_smem);
+    // this thread's row and chunk for ldmatrix; kBlock and D leave its bits 4..6 alone
+    const uint32_t at_q = sb_q + (lane & 7) * (D * 2) + (((lane >> 3) ^ (lane & 7)) << 4);
     const float sl2 = a.scale * kLog2e;
 
     for (; u < u_end; u++) {
@@ -127,7 +151,35 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
         if (!in && j0 < q.len && lane == 0) kv_flag(c.status);
         uint32_t kf[SETS][NG][4][4];                                     // operand: step m, register
         float2 sb[SETS][NG][2];                                          // scale, bias + 8 scale of entries g8, g8 + 8
-        {
+        if constexpr (MANY) {
+            // Columns 2 t4, 2 t4 + 1 of every 8, byte t4 of every word, as ldmatrix deals query
+            // rows to the threads: no block of them is put into another order.
+            const uint8_t* tile = c.pages + ((size_t)(in ? id : 0) * c.hkv + h) * (size_t)(4608 * NG);
+#pragma unroll
+            for (int g = 0; g < NG; g++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int e = (j0 + 8 * k + g8) % kKvPage;
+                    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    uint32_t f = 0;
+                    if (in) {
+                        w[0] = __ldg(reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32));
+                        w[1] = __ldg(reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32 + 16));
+                        f = __ldg(reinterpret_cast<const uint32_t*>(tile + 2048 * NG + (g * kKvPage + e) * 4));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int sel = t4 | (4 + t4) << 4;
+                        const uint4 x = codes_centred(__byte_perm(__byte_perm(w[i].x, w[i].y, sel), __byte_perm(w[i].z, w[i].w, sel), 0x5410));
+                        kf[0][g][2 * i][k] = __byte_perm(x.x, x.y, 0x5410);
+                        kf[0][g][2 * i][2 + k] = __byte_perm(x.z, x.w, 0x5410);
+                        kf[0][g][2 * i + 1][k] = __byte_perm(x.x, x.y, 0x7632);
+                        kf[0][g][2 * i + 1][2 + k] = __byte_perm(x.z, x.w, 0x7632);
+                    }
+                    const float2 v = h2f(f);
+                    sb[0][g][k] = make_float2(v.x, fmaf(8.f, v.x, v.y));
+                }
+        } else {
             const uint8_t* tile = c.pages + ((size_t)(in ? id : 0) * c.hkv + h) * (size_t)(4608 * NG);
             uint2 w[SETS][NG][2];
             uint32_t f[SETS][NG][2];
@@ -166,13 +218,66 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
         const int i0 = max(0, e0 - p0);
         const int i1 = a.window > 0 ? (int)min((long long)q.n - 1, (long long)min(e0 + UNIT, q.len) - 1 + a.window - 1 - p0) : q.n - 1;
         const int blk0 = i0 * G / kWtBlock, blk1 = i1 < i0 ? blk0 - 1 : (i1 * G + G - 1) / kWtBlock;
+        // MANY: query rows by 16-byte asynchronous copies, chunk x of row r at x ^ (r % 8); block
+        // i + 2 is on its way and the facts of block i + 1 are formed while block i is computed
+        const auto fetch = [&](int i) {
+            if (blk0 + i <= blk1) {
+                const int rr = (blk0 + i) * kWtBlock + (tid >> 2), at = min(rr, rows - 1);
+                const size_t row = q.first + at / G, head = h * G + at % G;
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + row * a.q_stride + head * D);
+                const uint32_t dst = sb_q + i % Sh::kBufs * Sh::kBlock + (tid >> 2) * (D * 2);
+#pragma unroll
+                for (int k = 0; k < 2 * NG; k++) {
+                    const int x = 4 * k + (tid & 3);
+                    cp_async16(dst + (x ^ ((tid >> 2) & 7)) * 16, src + x * 16, rr < rows);
+                }
+                if ((tid & 3) == 0) cp_async4(smem_u32(&s_lse[i % Sh::kBufs][tid >> 2]), a.lse + row * c.hq + head);
+            }
+            cp_async_commit();
+        };
+        const auto operand = [&](int y, int rt, int g, uint32_t (&b)[8]) {       // of 8 rows of buffer y, a group
+            const uint32_t at = y * Sh::kBlock + rt * 8 * (D * 2) + g * 128;
+            ldmatrix4(b[0], b[1], b[2], b[3], at_q + at);
+            ldmatrix4(b[4], b[5], b[6], b[7], (at_q ^ 64u) + at);
+        };
+        const auto facts = [&](int i) {              // sums of the queries, lse and positions
+            const int y = i % Sh::kBufs;
+#pragma unroll
+            for (int g = 0; g < NG; g++) {
+                uint32_t b[8];
+                operand(y, warp, g, b);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};   // a product with ones
+#pragma unroll
+                for (int m = 0; m < 4; m++) mma_f16(d, kOnes, kOnes, kOnes, kOnes, b[2 * m], b[2 * m + 1]);
+                if (g8 == 0) *reinterpret_cast<float2*>(&s_qs[y][warp][g][2 * t4]) = make_float2(d[0], d[1]);
+            }
+            if (tid < kWtBlock) {
+                const int rr = (blk0 + i) * kWtBlock + tid;
+                const float l = s_lse[y][tid];
+                s_lse[y][tid] = rr >= rows || l == -INFINITY ? INFINITY : l * kLog2e;   // such rows add nothing
+                s_pos[y][tid] = p0 + min(rr, rows - 1) / G;
+            }
+        };
+        if (MANY && blk0 <= blk1) {
+            fetch(0);
+            fetch(1);
+            cp_async_wait<1>();
+            __syncthreads();
+            facts(0);
+        }
         for (int blk = blk0; blk <= blk1; blk++) {
-            if (s != s_now || h != h_now || blk != blk_now) {            // alike in the whole CTA
+            const int i = blk - blk0, buf = MANY ? i % Sh::kBufs : 0;
+            if constexpr (MANY) {
+                cp_async_wait<0>();
+                __syncthreads();
+                fetch(i + 2);
+                if (blk < blk1) facts(i + 1);
+            } else if (s != s_now || h != h_now) {                       // alike in the whole CTA; one block
                 __syncthreads();
                 // query rows into operand order: thread 4 r + t takes 16 columns of each group of row r
-                const int t = tid & 3, r = tid >> 2, rr = blk * kWtBlock + r;
-                const bool on = rr < rows;
-                const int row = q.first + min(rr, rows - 1) / G, head = h * G + min(rr, rows - 1) % G;
+                const int t = tid & 3, r = tid >> 2;
+                const bool on = r < rows;
+                const int row = q.first + min(r, rows - 1) / G, head = h * G + min(r, rows - 1) % G;
                 const float lse_now = t == 0 && on ? a.lse[(size_t)row * c.hq + head] : -INFINITY;
 #pragma unroll
                 for (int g = 0; g < NG; g++) {
@@ -197,27 +302,32 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
                     }
                     qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
                     qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
-                    if (t == 0) s_qs[r >> 3][g][r & 7] = qsum;
+                    if (t == 0) s_qs[0][r >> 3][g][r & 7] = qsum;
                 }
                 if (t == 0) {
-                    s_lse[r] = lse_now == -INFINITY ? INFINITY : lse_now * kLog2e;   // such rows add nothing
-                    s_pos[r] = p0 + min(rr, rows - 1) / G;
+                    s_lse[0][r] = lse_now == -INFINITY ? INFINITY : lse_now * kLog2e;    // such rows add nothing
+                    s_pos[0][r] = p0 + min(r, rows - 1) / G;
                 }
                 s_now = s;
                 h_now = h;
-                blk_now = blk;
                 __syncthreads();
             }
             if (!in) continue;
             const int tiles = min(kWtBlock, rows - blk * kWtBlock + 7) / 8;
+            // whether every row of the block sees all of the entries
+            const int last = min(kWtBlock, rows - blk * kWtBlock) - 1;
+            const bool clear = s_pos[buf][0] >= j0 + 16 * SETS - 1 && (a.window == 0 || s_pos[buf][last] - a.window < j0);
             // PAIR row tiles side by side: their products and exponentials hide each other's latency
             constexpr int PAIR = MANY ? 2 : 1;
             for (int rt0 = warp / Sh::kGroups * PAIR; rt0 < tiles; rt0 += Sh::kSplit * PAIR) {
-                const int r0 = rt0 * 8, r1 = min(r0 + 8 * PAIR, rows - blk * kWtBlock) - 1;
-                const int pmin = s_pos[r0], pmax = s_pos[r1];
-                if (pmax < j0) continue;                                 // all before these entries
-                if (a.window > 0 && pmin - a.window + 1 > j0 + 16 * SETS - 1) continue;
-                const bool edge = j0 + 16 * SETS - 1 > pmin || (a.window > 0 && j0 < pmax - a.window + 1);
+                const int r0 = rt0 * 8;
+                bool edge = false;
+                if (!clear) {
+                    const int pmin = s_pos[buf][r0], pmax = s_pos[buf][min(r0 + 8 * PAIR, last + 1) - 1];
+                    if (pmax < j0) continue;                             // all before these entries
+                    if (a.window > 0 && pmin - a.window + 1 > j0 + 16 * SETS - 1) continue;
+                    edge = j0 + 16 * SETS - 1 > pmin || (a.window > 0 && j0 < pmax - a.window + 1);
+                }
                 float S[PAIR][SETS][4];
 #pragma unroll
                 for (int y = 0; y < PAIR; y++)
@@ -230,18 +340,25 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
 #pragma unroll
                     for (int y = 0; y < PAIR; y++) {
                         // rows behind the block's last are zero there, and add nothing
-                        const uint4 b0 = lds128(qb + (rt0 + y) * Sh::kQ + ((g * 2) * 32 + lane) * 16);
-                        const uint4 b1 = lds128(qb + (rt0 + y) * Sh::kQ + ((g * 2 + 1) * 32 + lane) * 16);
-                        const float2 qs = *reinterpret_cast<const float2*>(&s_qs[rt0 + y][g][2 * t4]);
+                        uint32_t b[8];
+                        if constexpr (MANY) {
+                            operand(buf, rt0 + y, g, b);
+                        } else {
+                            const uint4 b0 = lds128(sb_q + (rt0 + y) * Sh::kQ + ((g * 2) * 32 + lane) * 16);
+                            const uint4 b1 = lds128(sb_q + (rt0 + y) * Sh::kQ + ((g * 2 + 1) * 32 + lane) * 16);
+                            b[0] = b0.x; b[1] = b0.y; b[2] = b0.z; b[3] = b0.w;
+                            b[4] = b1.x; b[5] = b1.y; b[6] = b1.z; b[7] = b1.w;
+                        }
+                        const float2 qs = *reinterpret_cast<const float2*>(&s_qs[buf][rt0 + y][g][2 * t4]);
 #pragma unroll
                         for (int z = 0; z < SETS; z++) {
                             const uint32_t(&k)[4][4] = kf[z][g];
                             float(&S4)[4] = S[y][z];
                             float d[4];
-                            mma_f16(d, k[0][0], k[0][1], k[0][2], k[0][3], b0.x, b0.y, 0.f, 0.f, 0.f, 0.f);
-                            mma_f16(d, k[1][0], k[1][1], k[1][2], k[1][3], b0.z, b0.w);
-                            mma_f16(d, k[2][0], k[2][1], k[2][2], k[2][3], b1.x, b1.y);
-                            mma_f16(d, k[3][0], k[3][1], k[3][2], k[3][3], b1.z, b1.w);
+                            mma_f16(d, k[0][0], k[0][1], k[0][2], k[0][3], b[0], b[1], 0.f, 0.f, 0.f, 0.f);
+                            mma_f16(d, k[1][0], k[1][1], k[1][2], k[1][3], b[2], b[3]);
+                            mma_f16(d, k[2][0], k[2][1], k[2][2], k[2][3], b[4], b[5]);
+                            mma_f16(d, k[3][0], k[3][1], k[3][2], k[3][3], b[6], b[7]);
                             const float2 f0 = sb[z][g][0], f1 = sb[z][g][1];
                             S4[0] = fmaf(f0.x, d[0], fmaf(f0.y, qs.x, S4[0]));
                             S4[1] = fmaf(f0.x, d[1], fmaf(f0.y, qs.y, S4[1]));
@@ -251,14 +368,14 @@ __global__ void __launch_bounds__(kWtThreads, 2) k_attn_weights(const AttnArgs a
                     }
 #pragma unroll
                 for (int y = 0; y < PAIR; y++) {
-                    const float2 lse = *reinterpret_cast<const float2*>(&s_lse[r0 + 8 * y + 2 * t4]);
+                    const float2 lse = *reinterpret_cast<const float2*>(&s_lse[buf][r0 + 8 * y + 2 * t4]);
 #pragma unroll
                     for (int z = 0; z < SETS; z++) {
                         const float(&S4)[4] = S[y][z];
                         float w[4] = {exp2_fast(fmaf(S4[0], sl2, -lse.x)), exp2_fast(fmaf(S4[1], sl2, -lse.y)),
                                       exp2_fast(fmaf(S4[2], sl2, -lse.x)), exp2_fast(fmaf(S4[3], sl2, -lse.y))};
                         if (edge) {
-                            const int2 p = *reinterpret_cast<const int2*>(&s_pos[r0 + 8 * y + 2 * t4]);
+                            const int2 p = *reinterpret_cast<const int2*>(&s_pos[buf][r0 + 8 * y + 2 * t4]);
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 const int j = j0 + 16 * z + 8 * (k >> 1) + g8, at = k & 1 ? p.y : p.x;
