@@ -408,7 +408,7 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
         TileArgs y{a, kv->part, kv->cut, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
         const TileKernel k = tile_kernel(a.c.ng);
         KV_CK(kv_launch(1, k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
-        KV_CK(kv_launch(1, k.join, dim3(kv->n_sms, kTileRows / 32), kJoinThreads, 0, stream, y));
+        KV_CK(kv_launch(1, k.join, dim3(kv->n_sms, kTileRows / 32, a.c.ng), kJoinThreads, 0, stream, y));
     }
     if (!tile || a.c.n_seqs > 1) {
         const int rt = most <= 8 ? 1 : 2;

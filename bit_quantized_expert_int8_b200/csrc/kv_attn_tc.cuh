@@ -774,8 +774,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x: rows 32 blockIdx.y ..
-// of its tile, one per lane, 16 columns a warp at a time.
+// of its tile, one per lane, 64 columns a CTA, 8 a warp, eight parts at a time with
+// all their loads in flight (the weights first and then 16 columns a warp, two
+// passes where heads are wide, made a chunk of 128 rows over 4,096 entries of 256
+// columns 60 us; now 52).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 8;
 
 template <int NG>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const TileArgs x) {
@@ -785,45 +789,56 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const TileArgs x) {
     const TileCut c = x.cut[blockIdx.x];
     const int r = blockIdx.y * 32 + (threadIdx.x & 31), rr = c.rt * kTileRows + r;
     if (c.parts <= 0 || rr >= c.rows) return;
-    const int G = x.a.c.hq / x.a.c.hkv, head = c.h * G + rr % G;
-    // the first part is its CTA's second slot, the others their CTAs' first
-    const auto at = [&](int b) { return x.part + (size_t)(2 * ((int)blockIdx.x + b) + (b == 0 ? 1 : 0)) * kSlot; };
-    float M = -INFINITY, L = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < c.parts; b++) M = fmaxf(M, at(b)[kTileRows * D + r]);
-    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 8
-    for (int b = 0; b < c.parts; b++) {
-        const float mb = at(b)[kTileRows * D + r], lb = at(b)[kTileRows * D + kTileRows + r];
-        L = fmaf(mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref), lb, L);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const size_t row = (size_t)c.first + rr / G;
-    for (int col = (threadIdx.x >> 5) * 16; col < D; col += kJoinThreads / 32 * 16) {
-        float o[16];
+    const int col = blockIdx.z * 64 + (threadIdx.x >> 5) * 8;
+    float M = -INFINITY, L = 0.f, o[8];
 #pragma unroll
-        for (int e = 0; e < 16; e++) o[e] = 0.f;
-#pragma unroll 4
-        for (int b = 0; b < c.parts; b++) {
-            const float mb = at(b)[kTileRows * D + r], lb = at(b)[kTileRows * D + kTileRows + r];
-            const float f = mb == -INFINITY && lb == 0.f ? 0.f : exp2_fast(mb - ref);
+    for (int e = 0; e < 8; e++) o[e] = 0.f;
+    for (int b0 = 0; b0 < c.parts; b0 += kJoinParts) {
+        float m[kJoinParts], l[kJoinParts];
+        float4 v[kJoinParts][2];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float4 v = *reinterpret_cast<const float4*>(at(b) + ((size_t)(col / 4 + e) * kTileRows + r) * 4);
-                o[4 * e] = fmaf(f, v.x, o[4 * e]);
-                o[4 * e + 1] = fmaf(f, v.y, o[4 * e + 1]);
-                o[4 * e + 2] = fmaf(f, v.z, o[4 * e + 2]);
-                o[4 * e + 3] = fmaf(f, v.w, o[4 * e + 3]);
+        for (int k = 0; k < kJoinParts; k++) {
+            const int b = b0 + k;
+            m[k] = -INFINITY;
+            l[k] = 0.f;
+            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b < c.parts) {
+                // the first part is its CTA's second slot, the others their CTAs' first
+                const float* at = x.part + (size_t)(2 * ((int)blockIdx.x + b) + (b == 0 ? 1 : 0)) * kSlot;
+                m[k] = at[kTileRows * D + r];
+                l[k] = at[kTileRows * D + kTileRows + r];
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    v[k][e] = *reinterpret_cast<const float4*>(at + ((size_t)(col / 4 + e) * kTileRows + r) * 4);
             }
         }
-        __half* out = x.a.out + row * x.a.out_stride + (size_t)head * D + col;
+        float top = M;
 #pragma unroll
-        for (int e = 0; e < 2; e++)
-            *reinterpret_cast<uint4*>(out + 8 * e) =
-                make_uint4(f2h(o[8 * e] * inv, o[8 * e + 1] * inv), f2h(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                           f2h(o[8 * e + 4] * inv, o[8 * e + 5] * inv), f2h(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        for (int k = 0; k < kJoinParts; k++) top = fmaxf(top, m[k]);
+        const float ref = top == -INFINITY ? 0.f : top, back = exp2_fast(M - ref);
+        M = top;
+        L *= back;
+#pragma unroll
+        for (int e = 0; e < 8; e++) o[e] *= back;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; k++) {
+            const float f = m[k] == -INFINITY && l[k] == 0.f ? 0.f : exp2_fast(m[k] - ref);
+            L = fmaf(f, l[k], L);
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                o[4 * e] = fmaf(f, v[k][e].x, o[4 * e]);
+                o[4 * e + 1] = fmaf(f, v[k][e].y, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(f, v[k][e].z, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(f, v[k][e].w, o[4 * e + 3]);
+            }
+        }
     }
-    if (threadIdx.x < 32) x.a.lse[row * x.a.c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    const int G = x.a.c.hq / x.a.c.hkv, head = c.h * G + rr % G;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t row = (size_t)c.first + rr / G;
+    *reinterpret_cast<uint4*>(x.a.out + row * x.a.out_stride + (size_t)head * D + col) =
+        make_uint4(f2h(o[0] * inv, o[1] * inv), f2h(o[2] * inv, o[3] * inv), f2h(o[4] * inv, o[5] * inv), f2h(o[6] * inv, o[7] * inv));
+    if (col == 0) x.a.lse[row * x.a.c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace moeq4
