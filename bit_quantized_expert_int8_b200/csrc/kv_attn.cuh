@@ -44,8 +44,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // subnormals and first binade are linear in their bits, so a code in bits 0..3 is
 // the number code * 2^-24 as it stands and one in bits 4..7 is 16 times that: a
 // mask makes an operand, exactly, with no exponent to set and no offset to take
-// out again.  The factors 2^24 and 16 leave through the query operand (K) or the
-// sums (V).
+// out again.  The factors 2^24 and 16 leave through the query operand.
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&o)[4]) {
     const uint32_t u = w >> 8;
     o[0] = w & 0x000F000Fu;
@@ -126,8 +125,8 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 
 // ------------------------------------------------------- split attention --
-// Few rows per kv head (single tokens): bound by reading the cache, so every
-// byte of it is read once by one warp and used from registers.
+// Few rows per kv head (single tokens): every byte of the cache is read once per 8
+// or 16 rows by one warp and used from registers.
 //
 // An item is (sequence, tile of 8 RT rows, kv head); its rows are the
 // (row, query head) pairs that read the kv head, so a group's query heads share
@@ -140,9 +139,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 //   S = sum_g s_g (q_g . c_g) + b_g sum(q_g)
 // with tensor-core products of the raw codes (m16n8k16: rows = query rows,
 // columns = entries; q is taken times a power of two per row that brings its
-// largest to 1024..2048, so that 16 q, for the even pairs, stays exact), keeps a running
-// maximum (moved only when it grows by more than 2^8, so the sums are rescaled
-// rarely) and adds
+// largest to 1024..2048, so that 16 q, for the even pairs, stays exact), keeps a
+// running maximum (moved only when it grows by more than 2^8, so the sums are
+// rescaled rarely) and adds
 //   O += sum_j p_j s_jg (c_j - 8),   B_g += sum_j p_j (b_jg + 8 s_jg).
 // Codes of V are centred: raw ones (0..15) would let O grow to many times the
 // result, and the tensor cores' accumulation, which cuts off, would cost 8e-4 of it
@@ -152,16 +151,31 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // 2^-12 per entry on average; a second one for the remainder made the kernel 8 %
 // slower), kept in fp16's range by a power of two per warp (unit) that is chosen at
 // the first entries and lowered when a later p s would leave the range; it is part
-// of the exponent that p is formed with.  The warps' sums
-// meet in shared memory; an item cut by CTA borders goes through partial sums in
-// the workspace, joined in a fixed order by the last CTA to arrive (one counter
-// per item start, reset by that CTA).
+// of the exponent that p is formed with.  The warps' sums meet in shared memory; an
+// item cut by CTA borders goes through partial sums in the workspace, joined in a
+// fixed order by the last CTA to arrive (one counter per item start, reset by that
+// CTA).
+//
+// What bounds it is issue, about 690 instructions per 32 entries of 128 columns: 64
+// tokens with up to 16,384 entries take 169 us (3.6 TB/s of the cache, 0.56 of the
+// copy rate), one with 131,072 50 us (3.0 TB/s, the start and the join of the parts
+// included; the loop alone streams 4.6 TB/s).
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitStages = 2;        // 3 with 2 CTAs per SM: 100 us for 64 tokens, window 1024; 2 with 3: 84
-constexpr int kSplitMinUnits = 4;      // pages per CTA at least: fewer partial sums in small calls
+// Ring stages (and CTAs per SM below): 3 stages with 2 CTAs take 100 us for 64 tokens
+// with a window of 1024 (heads of 256), 2 with 3 take 84; 4 CTAs of 128 registers 5 %
+// more than 3 over long sequences of heads of 128.
+constexpr int kSplitStages = 2;
+// An item's start and end in pages.  64 tokens with up to 16,384 entries: 0 184 us, 2
+// to 8 alike (169).
 constexpr int kSplitItemCost = 4;
-constexpr int kSplitMaxRows = 16;      // (row, head) pairs per kv head: more go to the tile kernel
+// (row, head) pairs per kv head of a sequence; with more the tile kernel takes over.
+// This kernel reads the cache anew for every 16 of them, that one computes 128 whatever
+// there are: 16 sequences of up to 4,096 entries, heads of 128, here and there: 16 pairs
+// 36 and 97 us, 32 53 and 97, 64 84 and 99, 80 99 and 103; heads of 64, 64 pairs: 51 and
+// 79; of 256: 65 and 70.  (Over a few hundred entries of one sequence the tile kernel
+// would win from 32 on, 15 us against 18.)
+constexpr int kSplitMaxRows = 64;
 
 template <int NG, int RT>
 struct SplitShape {
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
         }
         total = warp_sum(total);
         const long long n = total + gridDim.x - 1;
-        const long long per = max(n >> 32 ? n / gridDim.x : (long long)((unsigned)n / gridDim.x), (long long)kSplitMinUnits);
+        const long long per = max(n >> 32 ? n / gridDim.x : (long long)((unsigned)n / gridDim.x), 1LL);
         const long long u = blockIdx.x * per;
         long long base = 0;
         if (u < total)

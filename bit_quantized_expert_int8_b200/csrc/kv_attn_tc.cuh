@@ -55,8 +55,11 @@ constexpr int kTileWarps = kTileSoft + kTileConv + 4;    // the issuer's warpgro
 constexpr int kTileSoftRegs = 112, kTileConvRegs = 104, kTileIssueRegs = 48;
 static_assert((kTileSoft * kTileSoftRegs + kTileConv * kTileConvRegs + 4 * kTileIssueRegs) <= kTileWarps * 96, "registers");
 constexpr int kTileThreads = kTileWarps * 32;
-constexpr int kTileItemCost = 4;       // pages an item costs beside its own
-constexpr int kTileMinUnits = 6;       // pages per CTA at least
+// Pages an item costs beside its own (0: 58 us for a chunk of 128 rows over 4,096
+// entries of 256 columns, 4 and 8: 52) and pages per CTA at least (64 rows of 4 heads
+// over 1,000 entries: 6 25 us, 3 to 1 20; a chunk of 128: 1 53 us, 2 52, 12 62).
+constexpr int kTileItemCost = 4;
+constexpr int kTileMinUnits = 2;
 constexpr int kTileMeta = 16;          // pages whose facts are kept for the softmax
 constexpr int kTileScales = 4;         // pages whose scales are kept for the converters
 constexpr float kTileLift = 6.f;       // p is taken times 2^6: at most 2^14 with a maximum 2^8 behind

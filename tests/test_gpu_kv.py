@@ -12,7 +12,7 @@ beside the half step 2^-11 of its rounding to fp16 (2^-25 below the normal
 range).
 
 One more operand is rounded to fp16, off by at most half a step, 2^-11 of its size.
-With up to 16 (row, head) pairs per kv head it is p s, the weight times a group's
+With up to 64 (row, head) pairs per kv head it is p s, the weight times a group's
 scale: an output is sum_j p_j s_j (code_j - 8) + p_j (bias_j + 8 s_j) over sum p, so
 it moves by at most 2^-11 sum_j w_j |s_j (code_j - 8)| with w = p / sum p.  With more
 it is V itself, scale * code + bias: at most 2^-11 sum_j w_j |v_j|.  Both are
@@ -101,7 +101,7 @@ class Case:
         return out, lse, got, spread
 
     def spread(self, s, q, K, V, scale, window, n):
-        few = q.shape[0] * self.Hq // self.Hkv <= 16
+        few = q.shape[0] * self.Hq // self.Hkv <= 64
         U = kv_ref.value_spread(self.pages, self.table[s], V, self.D) if few else np.abs(V)
         return kv_ref.attention(q.astype(np.float64), K, U, scale, window, n)[0]
 
@@ -151,6 +151,9 @@ SHAPES = [
     (128, 16, 1, [400], [40], 0),
     (128, 3, 1, [517], [200], 129),
     (256, 8, 8, [1100], [70], 600),
+    (128, 8, 2, [700, 65, 130], [16, 17, 5], 0),       # 64, 68 and 20 rows a kv head
+    (192, 7, 1, [450, 40], [9, 8], 30),                # 63 and 56
+    (64, 2, 2, [190, 70], [64, 65], 0),
 ]
 
 
