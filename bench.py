@@ -54,12 +54,13 @@ def parse():
     p.add_argument("--store-dir", default=tempfile.gettempdir(), help="directory of the expert file")
     p.add_argument("--store-layers", type=int, default=8, help="layers in the expert file")
     p.add_argument("--store-threads", type=int, default=16, help="pread threads")
-    p.add_argument("--workload", choices=("stack", "streaming", "batched", "prefill", "storage", "direct"),
+    p.add_argument("--workload", choices=("stack", "streaming", "batched", "prefill", "storage", "direct",
+                                        "attention"),
                    default="stack",
                    help="stack (default, the headline line), streaming (experts in pinned host "
                         "memory behind the LFU cache), batched (one layer, T tokens per step) or "
                         "prefill (streaming, the prompt in chunks) or storage (misses read "
-                        "from an expert file)")
+                        "from an expert file) or attention (decode steps on the 4-bit KV cache)")
     return p.parse_args()
 
 
@@ -868,6 +869,94 @@ def run_direct(args):
                       "kernels": "k_ffn_gateup_simple + k_ffn_down_simple"}), flush=True)
 
 
+def run_attention(args):
+    """Decode steps of one layer's attention on the 4-bit KV cache (32 query and
+    8 kv heads of 128): append the sequences' new rows, attend, and with a
+    budget also accumulate the weights and evict down to it, so the lengths
+    stay.  Caches filled by appends of random rows; two of them in turn, and
+    whether both exceed L2 is part of the line."""
+    import numpy as np
+    import torch
+
+    from bit_quantized_expert_int8_b200 import moeq4
+    from bit_quantized_expert_int8_b200.config import KvConfig
+    dev = torch.device("cuda", 0)
+    moeq4.load()
+    hbm, kind = peaks()
+    Hq, Hkv, D, page = 32, 8, 128, moeq4.MOE_KV_PAGE
+    for n, longest, budget in ((1, 512, 0), (1, 131072, 0), (64, 16384, 0), (16, 4097, 4096)):
+        rng = np.random.default_rng(SEED)
+        lens = rng.integers(max(1, longest // 32), longest + 1, n)
+        lens[0] = longest
+        if budget:
+            lens[:] = longest
+        mp = -(-longest // page)
+        states = []
+        for k in range(2):
+            cfg = KvConfig(Hq, Hkv, D, n * mp, mp, n, max(longest, n))
+            kv = moeq4.Kv(cfg)
+            t = dict(device=dev, dtype=torch.int32)
+            pages = torch.empty(n * mp * moeq4.kv_page_bytes(Hkv, D), dtype=torch.uint8, device=dev)
+            table = torch.as_tensor(rng.permutation(n * mp).reshape(n, mp), **t)
+            lens_d = torch.as_tensor(lens, **t)
+            seen = lens_d.clone()
+            opt = dict(score=torch.zeros((n, Hkv, mp * page), device=dev), pos=torch.zeros((n, Hkv, mp * page), **t),
+                       seen=seen) if budget else {}
+            for s in range(n):                                  # one sequence at a time
+                one = moeq4.KvCache(kv, pages, table[s], lens_d[s:s + 1],
+                                    **{k: v[s:s + 1] for k, v in opt.items()})
+                rows = torch.randn((2, int(lens[s]), Hkv, D), dtype=torch.float16, device=dev)
+                moeq4.moe_kv_append_q4(kv, one, moeq4.KvBatch(kv, torch.tensor([0, int(lens[s])], **t),
+                                                              int(lens[s]), int(lens[s])), *rows)
+            states.append(dict(kv=kv, lens=lens_d, seen=seen, q=torch.randn((n, Hq, D), dtype=torch.float16, device=dev),
+                               kvr=torch.randn((2, n, Hkv, D), dtype=torch.float16, device=dev),
+                               out=torch.empty((n, Hq, D), dtype=torch.float16, device=dev),
+                               cache=moeq4.KvCache(kv, pages, table, lens_d, **opt), new=torch.empty_like(lens_d),
+                               batch=moeq4.KvBatch(kv, torch.arange(n + 1, **t), n, 1)))
+
+        def step(st):
+            moeq4.moe_kv_append_q4(st["kv"], st["cache"], st["batch"], *st["kvr"])
+            moeq4.moe_attn_q4(st["kv"], st["cache"], st["batch"], st["q"], st["out"], scale=D ** -0.5,
+                              weights=budget > 0)
+            if budget:                                          # the next step's row stands behind what stays
+                moeq4.moe_kv_evict(st["kv"], st["cache"], n, budget, budget // 32, st["new"])
+                torch.add(st["new"], 1, out=st["lens"])
+                st["seen"].add_(1)
+
+        for st in states:
+            for _ in range(3):
+                step(st)
+        reps = 50
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        clocks = ClockSampler(0)
+        clocks.start()
+        runs = []
+        for _ in range(REPEATS):
+            torch.cuda.synchronize()
+            e0.record()
+            for i in range(reps):
+                step(states[i % 2])
+            e1.record()
+            torch.cuda.synchronize()
+            runs.append(e0.elapsed_time(e1) * 1000.0 / reps)
+        clk = clocks.stop()
+        for st in states:
+            moeq4.moe_kv_check(st["kv"])
+        us = statistics.median(runs)
+        entry = Hkv * moeq4.kv_page_bytes(1, D) // page         # an entry's K and V, codes, scales and biases
+        algo = int(lens.sum()) * entry
+        print(json.dumps({"metric": "decode tokens/s of one layer's attention", "workload": "attention",
+                          "sequences": n, "longest": longest, "entries": int(lens.sum()), "budget": budget or None,
+                          "value": round(n / us * 1e6, 1), "unit": "tokens/s", "us_per_step": round(us, 2),
+                          "us_min_max": [round(min(runs), 2), round(max(runs), 2)],
+                          "timing": f"median of {REPEATS} runs of {reps} steps, two caches in turn", "clocks": clk,
+                          "caches_exceed_l2": 2 * algo > 126e6,
+                          "cache_bytes_per_step": algo, "achieved_gbs": round(algo / us / 1e3, 1),
+                          "frac_of_hbm": round(algo / us / 1e3 / hbm, 4), "peak_kind": kind}), flush=True)
+        del states
+        torch.cuda.empty_cache()
+
+
 def main():
     args = parse()
     if args.impl == "reference":
@@ -882,6 +971,8 @@ def main():
         run_storage(args)
     elif args.workload == "direct":
         run_direct(args)
+    elif args.workload == "attention":
+        run_attention(args)
     else:
         run_ours(args)
 
