@@ -154,6 +154,9 @@ SHAPES = [
     (128, 8, 2, [700, 65, 130], [16, 17, 5], 0),       # 64, 68 and 20 rows a kv head
     (192, 7, 1, [450, 40], [9, 8], 30),                # 63 and 56
     (64, 2, 2, [190, 70], [64, 65], 0),
+    (64, 200, 1, [300, 70], [2, 1], 0),                # more heads than a tile has rows
+    (64, 1024, 1, [130], [1], 0),
+    (128, 8, 2, [300, 90], [1, 40], 2 ** 31 - 1),      # the widest window: all entries
 ]
 
 
@@ -476,6 +479,10 @@ def test_evict_orders(kind):
 
 def test_evict_many_entries_one_head():
     check_evict(Case(53, 64, 1, 1, [70000], [1], state=True), 30000, 1000)
+
+
+def test_evict_more_moves_than_a_list_holds():
+    check_evict(Case(54, 64, 1, 1, [140000], [1], state=True), 70000, 10)
 
 
 # ------------------------------------------------------ a run of them all --
