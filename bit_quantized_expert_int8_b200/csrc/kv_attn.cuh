@@ -84,6 +84,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// log sum exp of a row with total L = sum 2^(S - M).  The running maxima are whole
+// numbers (the next to the true one), so that they and the powers of two in the
+// totals add up exactly and only log2 of 1 <= L < 2 is rounded (with fractions left
+// in M and a large L the sum of the two cost lse 5e-7).
+__device__ __forceinline__ float lse_of(float M, float L) {
+    if (L == 0.f) return -INFINITY;
+    const int e = exponent_of(L);
+    return (M + (float)e + log2f(L * pow2(-e))) * kLn2;
+}
+
 // The same pairs as fp16 c - 8.
 __device__ __forceinline__ uint4 codes_centred(uint32_t w) {
     const uint32_t u = w >> 8;
@@ -298,7 +308,7 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int z = 0; z < RT; z++) {
-            const float m2 = fmaxf(A.m[z], top[z]);
+            const float m2 = rintf(fmaxf(A.m[z], top[z]));
             const float f = m2 == -INFINITY ? 1.f : exp2_fast(A.m[z] - m2);
             A.m[z] = m2;
             A.l[z] *= f;
@@ -689,7 +699,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
             v.z = f2h(o[4] * f, o[5] * f);
             v.w = f2h(o[6] * f, o[7] * f);
             *reinterpret_cast<uint4*>(a.out + (size_t)(q.first + i) * a.out_stride + (size_t)head * D + d) = v;
-            if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = lse_of(M, L);
         };
         const auto add = [](float (&o)[8], float f, float4 v0, float4 v1) {
             o[0] = fmaf(f, v0.x, o[0]); o[1] = fmaf(f, v0.y, o[1]);
@@ -785,7 +795,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
                     const float M = s_m[0][r], L = s_l[0][r], f = L == 0.f ? 0.f : 1.f / L;
                     *reinterpret_cast<uint2*>(a.out + (size_t)(q.first + i) * a.out_stride + (size_t)head * D + d) =
                         make_uint2(f2h(o.x * f, o.y * f), f2h(o.z * f, o.w * f));
-                    if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    if (d == 0) a.lse[(size_t)(q.first + i) * c.hq + head] = lse_of(M, L);
                 }
                 if (tid == 0) x.count[c0] = 0;
             }

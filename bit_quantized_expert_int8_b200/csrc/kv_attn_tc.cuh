@@ -7,7 +7,9 @@
 //   p = exp(S - max)            one row per pair of threads, P over S in tensor memory
 //   O[r][d] += P[r] . v[.][d]   tcgen05, P from tensor memory, V in shared memory
 // K enters as two fp16 operands, hi = fp16(s c + b) and lo = fp16(s c + b - hi),
-// so the scores are as exact as fp32 sums are.  (With the raw codes as operands
+// so the scores are as exact as fp32 sums are; the products of lo come first, because
+// the tensor cores cut off at the size of the running sum (hi first: twice the error of
+// lse, 1.8e-7 of it instead of 0.9e-7 with heads of 256).  (With the raw codes as operands
 // and the groups' scales folded in by the softmax threads, as the few-row kernel
 // does it, every thread reads every entry's scales from shared memory: 512
 // 16-byte broadcasts a tile, 427 us against 334 at 4 chunks of 512.)  p enters as
@@ -62,7 +64,7 @@ constexpr int kTileItemCost = 4;
 constexpr int kTileMinUnits = 2;
 constexpr int kTileMeta = 16;          // pages whose facts are kept for the softmax
 constexpr int kTileScales = 4;         // pages whose scales are kept for the converters
-constexpr float kTileLift = 6.f;       // p is taken times 2^6: at most 2^14 with a maximum 2^8 behind
+constexpr float kTileLift = 6.f;       // p is taken times 2^6: at most 2^14.5 with a maximum 2^8.5 behind
 
 template <int NG>
 struct TileShape {
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const float du = meta.vexp - vexp;       // V's unit moved (alike in all threads)
                 const bool grow = top > m + 8.f;
                 if (__any_sync(0xffffffffu, grow) || du != 0.f) {
-                    const float m2 = grow ? top : m;
+                    const float m2 = grow ? rintf(top) : m;
                     const float fp = m2 == -INFINITY ? 1.f : exp2_fast(m - m2), f = fp * exp2f(du);
                     m = m2;
                     vexp = meta.vexp;
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 }
                 if (half == 0 && row) {
                     if (sg.whole) {
-                        a.lse[(size_t)(sg.first + rr / G) * c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                        a.lse[(size_t)(sg.first + rr / G) * c.hq + head] = lse_of(M, L);
                     } else {
                         slot[kTileRows * D + r] = M;
                         slot[kTileRows * D + kTileRows + r] = L;
@@ -739,13 +741,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 tc_fence_after();
                 const uint32_t dk = (uint32_t)tc_sdesc_sw128(sK + (n % KR) * Sh::kK), ds = tmem + Sh::kS + st * KT;
 #pragma unroll
-                for (int z = 0; z < 2; z++)              // hi, lo
+                for (int z = 0; z < 2; z++)              // lo, then hi
 #pragma unroll
                     for (int g = 0; g < NG; g++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             const uint32_t da = tmem + Sh::kQ + g * 32 + 8 * k;
-                            const uint64_t db = tc_desc(dk + (((z * NG + g) * KT * 128) >> 4) + 2u * k, dhi);
+                            const uint64_t db = tc_desc(dk + ((((1 - z) * NG + g) * KT * 128) >> 4) + 2u * k, dhi);
                             if (z + g + k == 0) tc_mma_ts(ds, da, db, id_s, 0u);
                             else tc_mma_ts_acc(ds, da, db, id_s);
                         }
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const TileArgs x) {
     const size_t row = (size_t)c.first + rr / G;
     *reinterpret_cast<uint4*>(x.a.out + row * x.a.out_stride + (size_t)head * D + col) =
         make_uint4(f2h(o[0] * inv, o[1] * inv), f2h(o[2] * inv, o[3] * inv), f2h(o[4] * inv, o[5] * inv), f2h(o[6] * inv, o[7] * inv));
-    if (col == 0) x.a.lse[row * x.a.c.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (col == 0) x.a.lse[row * x.a.c.hq + head] = lse_of(M, L);
 }
 
 }  // namespace moeq4
