@@ -414,6 +414,10 @@ k_kv_evict(const KvArgs a, int budget, int n_recent, int32_t* __restrict__ new_l
         mb += r < me ? s_mc[r] : 0;
         moves += s_mc[r];
     }
+    if (moves == 0) {                                           // alike in the whole cluster
+        cluster.sync();                                         // nobody leaves while its counts are being read
+        return;
+    }
     const int share = (moves + C - 1) / C, room = evict_room(part_cap);
     const KvTile t(a.ng);
     // 2^sh lanes a move: 4 ng of them copy 16 bytes of codes, 2 ng a scale and bias, two the

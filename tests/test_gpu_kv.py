@@ -485,6 +485,43 @@ def test_evict_more_moves_than_a_list_holds():
     check_evict(Case(54, 64, 1, 1, [140000], [1], state=True), 70000, 10)
 
 
+@pytest.mark.parametrize("kind", ["equal", "descending", "ascending", "ties", "zeros", "nan", "all recent", "one move"])
+@pytest.mark.parametrize("entries", [4500, 8300, 16500])        # clusters of 2, 4 and 8 CTAs
+def test_evict_orders_across_parts(entries, kind):
+    """Orders whose borders, ties or lack of any move lie across the parts of a cluster."""
+    c = Case(55, 64, 2, 2, [entries, entries - 300], [1, 1], state=True)
+    s, budget, recent = c.score, entries // 2 + 5, 0
+    if kind == "equal":                                          # the first `budget` entries stay: nothing moves
+        s[:] = 0.25
+    elif kind == "descending":
+        s[:] = -np.arange(c.cap, dtype=np.float32)
+    elif kind == "ascending":                                    # as many moves as there can be
+        s[:] = np.arange(c.cap, dtype=np.float32)
+    elif kind == "ties":
+        s[:] = np.floor(s * 3)
+    elif kind == "zeros":
+        s[:] = np.where(s < 0.9, np.where(s < 0.4, 0.0, -0.0), s)
+    elif kind == "nan":
+        s[:] = np.where(s < 0.6, np.float32(np.nan), s)
+        s[1, 0] = np.nan
+    elif kind == "all recent":
+        c.pos[:] = 3 * entries
+        recent = budget
+    else:
+        s[:] = 0.25
+        s[:, :, 3] = 0.0
+        s[1, 1, 3] = 0.25                                        # and one (sequence, head) without any
+    c.upload()
+    check_evict(c, budget, recent)
+    if kind in ("equal", "descending"):                          # nothing has changed: the same again, many times
+        new = torch.zeros(c.n, dtype=torch.int32, device=DEV)
+        for _ in range(50):
+            moeq4.moe_kv_evict(c.kv, c.cache, c.n, budget, recent, new)
+        moeq4.moe_kv_check(c.kv)
+        for name in ("pos", "score", "pages"):
+            assert np.array_equal(c.g[name].cpu().numpy(), getattr(c, name))
+
+
 # ------------------------------------------------------ a run of them all --
 def test_bounded_decode_steps():
     """Prompt chunk, then decode steps with a bounded cache: append, attention
