@@ -401,7 +401,9 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.scale = scale;
-    a.window = window;
+    // as wide as the cache: every entry is seen, as without a window.  (Narrower ones keep
+    // "entry - window" of rows before the first entry within 32 bits.)
+    a.window = window < kv->cfg.max_pages * kKvPage ? window : 0;
     // sequences of many rows on the tile kernel, of few on the split kernel (each passes over
     // the other's); one sequence needs one of them
     const int64_t most = (int64_t)a.c.max_q * (a.c.hq / a.c.hkv);

@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<NG, RT>::kCtas) k_at
 
     while (u < u_end) {
         while (u >= s_base + q.units) {                      // sequences without units are passed over
+            if (s + 1 >= c.n_seqs) return;                   // (not reached while what lens says stays)
             s_base += q.units;
             s++;
             q = split_seq<R>(x, s, false);

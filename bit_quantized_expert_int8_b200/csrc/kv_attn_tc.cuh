@@ -198,6 +198,7 @@ struct TileWalk {
             int plo, np;
             while (true) {                                       // row tile that holds unit u
                 while (rt >= q.tiles) {
+                    if (s + 1 >= c.n_seqs) return g;             // (not reached while what lens says stays)
                     base += q.units;
                     q = tile_seq(x, ++s, false);
                     rt = 0;

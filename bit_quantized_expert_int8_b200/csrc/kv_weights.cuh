@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kWtThreads, WtShape<NG, MANY>::kCtas) k_attn_w
 
     for (; u < u_end; u++) {
         while (u >= base + (long long)q.units * c.hkv) {
+            if (s + 1 >= c.n_seqs) return;                       // (not reached while what lens says stays)
             base += (long long)q.units * c.hkv;
             s++;
             q = wt_seq<UNIT>(a, s);

@@ -182,6 +182,21 @@ def test_attention_weights(D, Hq, Hkv, lens, rows, window):
         assert np.array_equal(got[s, :, lens[s]:], c.score[s, :, lens[s]:].astype(np.float64))
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 64, 64, 3])
+@pytest.mark.parametrize("Hq,lens,rows", [(4, [2, 40], [5, 1]), (4, [30, 0, 100], [60, 5, 7]), (16, [70, 5], [200, 9])])
+def test_window_with_rows_before_the_first_entry(Hq, lens, rows, window):
+    """Rows that stand before the first entry see nothing, those behind them all
+    that the window shows, however wide it is."""
+    c = Case(13 + Hq + sum(lens), 128, Hq, 2, lens, rows, state=True)
+    q = c.queries()
+    ref = c.reference(q, 0.09, window)
+    out, lse = c.attend(q, 0.09, window, weights=True)
+    close(out, lse, ref)
+    want = c.score.astype(np.float64) + ref[2]
+    got = c.g["score"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= 1e-4 * ref[2] + 2.0 ** -23 * np.abs(want) + 1e-6).all(), np.abs(got - want).max()
+
+
 def test_long_sequences_and_split_work():
     c = Case(21, 128, 16, 4, [9000, 3, 2500, 640], [1, 1, 1, 1], state=True)
     q = c.queries()
