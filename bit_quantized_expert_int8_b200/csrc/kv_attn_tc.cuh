@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             const auto load_k = [&](const uint8_t* tile) {
 #pragma unroll
                 for (int i = 0; i < NK; i++)
-                    if (i * CT + ct < 128 * NG) rk[i] = __ldg(reinterpret_cast<const uint4*>(tile) + i * CT + ct);
+                    if (i * CT + ct < 128 * NG) rk[i] = reinterpret_cast<const uint4*>(tile)[i * CT + ct];
             };
             const auto load_v = [&](const uint8_t* tile) {
 #pragma unroll
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     const uint8_t* v = tile + 2304 * NG + (n >> 7) * 2048 + ((n >> 4) & 7) * 256 + ((n >> 1) & 7) * 4;
                     if (n < 128 * NG)
 #pragma unroll
-                        for (int e = 0; e < 8; e++) rv[i][e] = __ldg(reinterpret_cast<const uint32_t*>(v + e * 32));
+                        for (int e = 0; e < 8; e++) rv[i][e] = *reinterpret_cast<const uint32_t*>(v + e * 32);
                 }
             };
             int id = page_at(0), id2 = page_at(1);       // pages t and t + 1
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 if (held && !there && v == 0 && lane == 0) kv_flag(c.status);
                 const uint8_t* at = c.pages + ((size_t)(there ? id : 0) * c.hkv + sg.h) * (size_t)(4608 * NG) + (2304 * v + 2048) * NG;
 #pragma unroll
-                for (int i = 0; i < N; i++) f[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i * 32 + lane);
+                for (int i = 0; i < N; i++) f[i] = reinterpret_cast<const uint32_t*>(at)[i * 32 + lane];
             };
             int vexp = 0;                                // log2 of V's factor
             float vtop = 0.f;                            // largest value it admits

@@ -36,6 +36,9 @@ struct KvArgs {
 
 // The kernels of a decode step follow one another closely: each lets the next
 // be scheduled early and waits here for the work before it, so launches overlap.
+// What other kernels of the stream write (pages, rows, lse) is therefore read with
+// ordinary or L2 loads only: this kernel may be resident while it is written, and
+// loads through the read-only path are not ordered behind the wait.
 __device__ __forceinline__ void kv_begin() {
     griddep_launch_dependents();
     griddep_wait();

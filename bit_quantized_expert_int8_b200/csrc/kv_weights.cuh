@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(kWtThreads, WtShape<NG, MANY>::kCtas) k_attn_w
                     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                     uint32_t f = 0;
                     if (in) {
-                        w[0] = __ldg(reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32));
-                        w[1] = __ldg(reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32 + 16));
-                        f = __ldg(reinterpret_cast<const uint32_t*>(tile + 2048 * NG + (g * kKvPage + e) * 4));
+                        w[0] = *reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32);
+                        w[1] = *reinterpret_cast<const uint4*>(tile + (g * kKvPage + e) * 32 + 16);
+                        f = *reinterpret_cast<const uint32_t*>(tile + 2048 * NG + (g * kKvPage + e) * 4);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kWtThreads, WtShape<NG, MANY>::kCtas) k_attn_w
                         w[z][g][k] = make_uint2(0, 0);
                         f[z][g][k] = 0;
                         if (in) {
-                            w[z][g][k] = __ldg(reinterpret_cast<const uint2*>(tile + (g * kKvPage + e) * 32 + t4 * 8));
-                            f[z][g][k] = __ldg(reinterpret_cast<const uint32_t*>(tile + 2048 * NG + (g * kKvPage + e) * 4));
+                            w[z][g][k] = *reinterpret_cast<const uint2*>(tile + (g * kKvPage + e) * 32 + t4 * 8);
+                            f[z][g][k] = *reinterpret_cast<const uint32_t*>(tile + 2048 * NG + (g * kKvPage + e) * 4);
                         }
                     }
 #pragma unroll

@@ -670,6 +670,44 @@ def test_many_ragged_sequences(seed):
     assert (np.abs(got - want) <= 1e-4 * ref[2] + 2.0 ** -23 * np.abs(want) + 1e-6).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,lens,rows", [(128, 8, 2, [700, 300], [1, 1]), (128, 8, 2, [300, 129], [40, 33]),
+                                                (256, 4, 2, [200, 64], [50, 3])])
+def test_calls_behind_one_another_see_what_was_written(D, Hq, Hkv, lens, rows):
+    """Appends and attentions in one graph, launches overlapping, nothing between
+    them: each attention sees the rows just written, also where an earlier one
+    has read the same entries."""
+    c = Case(73, D, Hq, Hkv, lens, rows, state=True)
+    m, n = 12, c.n_rows
+    k, v = (c.rng.standard_normal((2, m, n, Hkv, D)) * 1.2).astype(np.float16)
+    k, v, q = cu(k), cu(v), cu(c.queries())
+
+    def outputs():
+        return torch.zeros((m, n, Hq, D), dtype=torch.float16, device=DEV), torch.zeros((m, n, Hq), device=DEV)
+
+    def step(i, out, lse):
+        moeq4.moe_kv_append_q4(c.kv, c.cache, c.batch, k[i], v[i])
+        moeq4.moe_attn_q4(c.kv, c.cache, c.batch, q, out[i], lse=lse[i], scale=0.09, weights=True)
+
+    alone, got = outputs(), outputs()
+    score = c.g["score"].clone()
+    for i in range(m):
+        step(i, *alone)
+        torch.cuda.synchronize()
+    after = c.g["score"].clone()
+    assert not torch.equal(alone[0][0], alone[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(m):
+            step(i, *got)
+    for _ in range(20):
+        c.g["score"].copy_(score)
+        got[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], alone[0]) and torch.equal(got[1], alone[1]) and torch.equal(c.g["score"], after)
+    moeq4.moe_kv_check(c.kv)
+
+
 def test_two_contexts_on_two_streams():
     """Calls of two contexts at once give what each gives alone."""
     cs = [Case(67, 128, 8, 2, [3000, 700], [1, 60], state=True), Case(68, 128, 16, 4, [900, 2000], [150, 1], state=True)]

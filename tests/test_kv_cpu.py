@@ -1,6 +1,8 @@
 """4-bit KV cache, host side: sizes, refusals that need no GPU, and pins of the
 64-bit reference that the GPU tests compare with."""
 import ctypes
+import os
+import re
 import types
 
 import numpy as np
@@ -132,3 +134,14 @@ def test_reference_eviction_by_hand():
     assert pos[0, :6].tolist() == [0, 4, 2, 5, 4, 5]
     assert score[0, :4].tolist() == [5, 1, 3, 0]
     assert [kv_ref.entry(pages[0, 0], D, 1, e)[0] for e in range(6)] == [0, 4, 2, 5, 4, 5]
+
+
+def test_kernels_read_memory_coherently():
+    """Every kernel of the KV cache may be resident while the work before it runs:
+    none reads global memory through the read-only path (whose loads are not
+    ordered behind the wait), by name or by const __restrict__."""
+    for path in build.sources():
+        if os.path.basename(path).startswith("kv_"):
+            with open(path) as f:
+                text = re.sub(r"//.*", "", f.read())
+            assert not re.search(r"__ldg|\.nc\b|const[^;(),]*\*\s*__restrict__", text), path
