@@ -160,7 +160,8 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // stand, and 8 query rows fill a tile.  p s enters as one fp16 value (a relative
 // 2^-12 per entry on average; a second one for the remainder made the kernel 8 %
 // slower), kept in fp16's range by a power of two per warp (unit) that is chosen at
-// the first entries and lowered when a later p s would leave the range; it is part
+// the first entries and lowered when a later p s would leave the range, so that p s is
+// held to 2^-29 of the largest that the warp's rows have met; it is part
 // of the exponent that p is formed with.  The warps' sums meet in shared memory; an
 // item cut by CTA borders goes through partial sums in the workspace, joined in a
 // fixed order by the last CTA to arrive (one counter per item start, reset by that
@@ -362,7 +363,8 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
         };
         const bool fits = parts();
         if (__any_sync(0xffffffffu, !fits || !A.chosen)) {
-            // the unit becomes the one that brings the largest p s to 16..32
+            // the unit becomes the one that brings the largest finite p s to 16..32 (an infinite
+            // one belongs to the rows that see it, and must not keep the others' in fp16's way)
             float mx = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; g++)
@@ -370,10 +372,13 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
                 for (int z = 0; z < RT; z++)
 #pragma unroll
                     for (int k = 0; k < 4; k++)
-                        if (seen(z, k)) mx = fmaxf(mx, fabsf(p[z][4 * b + k] * h2f(sb[g][k]).x));
+                    {
+                        const float v = p[z][4 * b + k] * h2f(sb[g][k]).x;
+                        if (seen(z, k)) mx = fmaxf(mx, fabsf(fmaf(v, 0.f, v)));  // v, or NaN, which fmaxf passes over
+                    }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (mx > 0.f && mx < 1e30f) {                // else nothing here, or nothing finite to keep
+            if (mx > 0.f) {                              // else nothing here, or nothing finite to keep
                 const float du = fmaxf(fminf(4.f - floorf(log2f(mx)), 60.f - A.unit), -60.f - A.unit);
                 const float f = exp2f(du);
                 A.unit += du;

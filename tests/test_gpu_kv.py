@@ -307,6 +307,43 @@ def test_nan_reaches_only_the_rows_that_see_it():
     assert np.isnan(out[15:, 2:]).all() and np.isnan(lse[15:, 2:]).all()
 
 
+def scale_v(pages, table, j, factor, groups=(0, 1)):
+    """Entry j's V times a factor (its scales and biases; 128 columns, all kv heads)."""
+    for g in groups:
+        o = 2304 * 2 + 2048 * 2 + (g * 64 + j % 64) * 4
+        sb = pages[table[j // 64], :, o:o + 4].copy().view(np.float16).astype(np.float64)
+        with np.errstate(over="ignore"):
+            pages[table[j // 64], :, o:o + 4] = (sb * factor).astype(np.float16).view(np.uint8)
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("rows", [8, 16, 30, 70, 140])          # 8 and 16 rows a tile, 128 on the tile kernel
+def test_v_out_of_range_stays_with_the_rows_that_see_it(rows, bad):
+    """The last entry's V is not finite, in one group of 64 columns: other rows, and
+    the last row's other group, stay right beside V whose scale is near the largest."""
+    c = Case(76, 128, 2, 2, [400], [rows])
+    tile = c.pages[c.table[0, 6]]                                # entries 384 to 399
+    ng = 2
+    for g in range(ng):
+        o = 2304 * ng + g * 2048
+        tile[:, o + 32:o + 16 * 32] &= 0x11                      # codes 0 and 1
+        o = 2304 * ng + 2048 * ng + g * 256
+        tile[:, o + 4:o + 16 * 4] = np.tile(np.array([50000, 0], np.float16).view(np.uint8), 15)
+    q = c.queries()
+    ref = c.reference(q, 0.09)
+    o = 2304 * ng + 2048 * ng + 15 * 4
+    tile[:, o:o + 4] = np.array([bad, 0], np.float16).view(np.uint8)
+    c.upload()
+    out, lse = c.attend(q, 0.09)
+    assert not np.isfinite(out[-1, :, :64]).any()
+    out[-1, :, :64] = ref[0][-1, :, :64]
+    assert np.isfinite(out).all()
+    # 2^-11 of the spread, and sums of 16-entry steps as in the tolerances above, of values
+    # 50000 times as large
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 1e-4 * 50000).all()
+    assert (np.abs(lse - ref[1]) <= 1e-4).all()
+
+
 def test_rows_behind_the_last_sequence_stay():
     for rows in ([1, 2], [40, 3]):
         c = Case(28, 128, 8, 2, [200, 90], rows, spare_rows=5)
