@@ -388,7 +388,11 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: q and out overlap", who);
     if (flags & ~MOE_ATTN_WEIGHTS) return kv_fail(MOE_ERR_INVALID_ARG, "%s: unknown flags 0x%x", who, flags);
     if (window < 0) return kv_fail(MOE_ERR_INVALID_ARG, "%s: window must be >= 0", who);
-    if (!std::isfinite(scale)) return kv_fail(MOE_ERR_INVALID_ARG, "%s: scale must be finite", who);
+    // the kernels multiply it by powers of two between 2^-37 and 2^25 and by sums below 2^46:
+    // neither the factors (0 times the -infinity of a masked entry) nor the scores leave fp32
+    const float mag = std::fabs(scale);
+    if (!(scale == 0.f || (mag >= 0x1p-32f && mag <= 0x1p32f)))
+        return kv_fail(MOE_ERR_INVALID_ARG, "%s: scale must be 0 or between 2^-32 and 2^32 in size", who);
     if ((flags & MOE_ATTN_WEIGHTS) && !cache->score)
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: MOE_ATTN_WEIGHTS needs cache->score", who);
     if (!kv_al(lse, 4)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: misaligned lse", who);

@@ -611,6 +611,8 @@ int moe_kv_read_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch,
  *   q    device fp16 [n_rows][n_q_heads][head_dim], out likewise; they must not
  *        overlap (both may be columns of the same rows)
  *   lse  device fp32 [n_rows][n_q_heads] or NULL
+ *   scale  0, or 2^-32 to 2^32 in size.  Scores S_j of 2^28 and more in size are not
+ *        served (their rounding to fp32 would pass the exponents of exp)
  * flags & MOE_ATTN_WEIGHTS: also adds to cache->score, for every entry j and
  * kv head, sum exp(S_j - lse) over the sequence's rows and the kv head's query
  * heads (each score is written once, in a fixed order: repeated runs agree bit

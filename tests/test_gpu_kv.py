@@ -224,6 +224,32 @@ def test_scales(scale):
     close(out, lse, c.reference(q, scale))
 
 
+@pytest.mark.parametrize("rows", [[1, 9], [40, 70]])
+@pytest.mark.parametrize("scale", [2.0 ** -32, -(2.0 ** 32), 2.0 ** 32])
+def test_smallest_and_largest_scales(scale, rows):
+    """The least scale makes every entry count alike, the largest one leaves one entry a row."""
+    c = Case(74, 128, 8, 2, [200, 90], rows)
+    q = c.queries()
+    if abs(scale) > 1:                                           # scores of a few million: below 2^28
+        q = (q.astype(np.float64) * 2.0 ** -14).astype(np.float16)
+    ref = c.reference(q, scale)
+    out, lse = c.attend(q, scale)
+    rl = ref[1]
+    # lse is as large as the scores are: their partial sums (at most 40, see above) are
+    # rounded a few dozen times, which is below 1e-5 of a score of a few units
+    assert (np.abs(lse - rl) <= 1e-4 + 1e-5 * np.abs(rl)).all()
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 2.0 ** -25 + 1e-4).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -33, -1e-30, 2.0 ** 33, -3e38, 1e-45])
+def test_scales_out_of_range_are_refused(scale):
+    c = Case(75, 128, 8, 2, [20], [2])
+    q = cu(c.queries())
+    out = torch.full_like(q, 7)
+    refused(moeq4.MOE_ERR_INVALID_ARG, moeq4.moe_attn_q4, c.kv, c.cache, c.batch, q, out, scale=scale)
+    assert (out == 7).all()
+
+
 @pytest.mark.parametrize("sigma", [1e-4, 300.0])
 def test_small_and_large_values(sigma):
     """V of any size: the output's error scales with it."""
