@@ -77,8 +77,8 @@ struct moe_kv {
     int* count = nullptr;      // arrivals per cut item, zero between calls
     int split_ctas[2] = {0, 0};  // CTAs of the split kernel: 8-row and 16-row tiles
     int split_smem[2] = {0, 0};
-    size_t counts = 0;         // length of count
     TileCut* cut = nullptr;    // [n_sms]
+    unsigned long long wait_ns = kWaitNs;  // bound of the tile kernel's waits
 };
 
 // The split kernel of one head size and row-tile count.
@@ -215,7 +215,6 @@ extern "C" int moe_kv_create(const MoeKvConfig* cfg, moe_kv** out) {
     }
     const size_t o_part = take(part * sizeof(float));
     const size_t o_count = take(ctas * sizeof(int));
-    kv->counts = ctas;
     const size_t o_cut = take((size_t)kv->n_sms * sizeof(TileCut));
     for (int many = 0; many < 2; many++) {
         const WtKernel k = weights_kernel(cfg->head_dim / 64, many);
@@ -262,11 +261,17 @@ extern "C" int moe_kv_check(moe_kv* kv, moe_stream_t stream) {
     KV_CK(cudaStreamSynchronize(stream));
     if (st[0] == 0 && st[1] == 0) return MOE_OK;
     KV_CK(cudaMemsetAsync(kv->status, 0, sizeof(st), stream));
-    if (st[1] != 0) {                  // some CTAs left early: the arrival counts begin anew
-        KV_CK(cudaMemsetAsync(kv->count, 0, kv->counts * sizeof(int), stream));
+    if (st[1] != 0)                    // (the tile kernel's; the split kernel and its counts wait for nobody)
         return kv_fail(st[1], "a bounded device wait of an attention call gave up; its outputs are not valid");
-    }
     return kv_fail(st[0], "a KV cache kernel met a length, row start or page index outside its limits");
+}
+
+extern "C" int moe_kv_set_wait_ns(moe_kv* kv, unsigned long long ns) {
+    if (!kv) return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_set_wait_ns: NULL context");
+    if (ns < 1000ull || ns > 60000000000ull)
+        return kv_fail(MOE_ERR_INVALID_ARG, "moe_kv_set_wait_ns: %llu ns outside 1 us .. 60 s", ns);
+    kv->wait_ns = ns;
+    return MOE_OK;
 }
 
 static int kv_check_cache(const moe_kv* kv, const MoeKvCache* c, int n_seqs, const char* who) {
@@ -413,7 +418,7 @@ extern "C" int moe_attn_q4(moe_kv* kv, const MoeKvCache* cache, const MoeKvBatch
     const int64_t most = (int64_t)a.c.max_q * (a.c.hq / a.c.hkv);
     const bool tile = most > kSplitMaxRows;
     if (tile) {
-        TileArgs y{a, kv->part, kv->cut, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1};
+        TileArgs y{a, kv->part, kv->cut, a.c.n_seqs == 1 ? 0 : kSplitMaxRows + 1, kv->wait_ns};
         const TileKernel k = tile_kernel(a.c.ng);
         KV_CK(kv_launch(1, k.fn, dim3(kv->n_sms), kTileThreads, k.smem, stream, y));
         KV_CK(kv_launch(1, k.join, dim3(kv->n_sms, kTileRows / 32, a.c.ng), kJoinThreads, 0, stream, y));

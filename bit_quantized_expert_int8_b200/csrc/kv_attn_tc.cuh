@@ -99,6 +99,7 @@ struct TileArgs {
     float* part;               // [2 gridDim.x][128 (D + 2)]: sums, then maximum and total per row
     TileCut* cut;              // [gridDim.x]: the cut item that begins in each CTA
     int min_rows_seq;          // sequences with fewer (row, head) pairs per kv head are not served here
+    unsigned long long wait_ns; // bound of every wait inside the kernel
 };
 
 struct TileSeq {
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const uint32_t n = gt + t;
                 const int st = n & 1;
                 const uint32_t t_s = t_row + Sh::kS + st * KT;
-                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_s[st], (n >> 1) & 1u, c.stop));
+                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_s[st], (n >> 1) & 1u, c.stop, x.wait_ns));
                 if (!ok) {                               // the other half may still come to the barrier
                     named_bar(1 + q4, 64);
                     continue;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     vexp = meta.vexp;
                     l *= fp;
                     if (t > 0) {                         // O so far: this half's columns of the row
-                        ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(n - 1) % VR], ((n - 1) / VR) & 1u, c.stop));
+                        ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(n - 1) % VR], ((n - 1) / VR) & 1u, c.stop, x.wait_ns));
                         if (!ok) continue;
                         tc_fence_after();
 #pragma unroll
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 #pragma unroll
             for (int g = 0; g < NG; g++) s_sum[half][g][r] = poison[g];
             named_bar(1 + q4, 64);
-            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(gt + T - 1) % VR], ((gt + T - 1) / VR) & 1u, c.stop));
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[(gt + T - 1) % VR], ((gt + T - 1) / VR) & 1u, c.stop, x.wait_ns));
             tc_fence_after();
             if (ok) {
                 const float L = s_sum[0][NG][r] + s_sum[1][NG][r];
@@ -541,8 +542,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const int sl = n % kTileScales;
                 // the page's scales, and K's slot once Q K of the slot's last page has ended
                 if (ok)
-                    ok = __all_sync(0xffffffffu, wait_bar(&b_sc[sl], (n / kTileScales) & 1u, c.stop) &&
-                                                     (n < KR || wait_bar(&b_kf[n % KR], ((n / KR) - 1) & 1u, c.stop)));
+                    ok = __all_sync(0xffffffffu, wait_bar(&b_sc[sl], (n / kTileScales) & 1u, c.stop, x.wait_ns) &&
+                                                     (n < KR || wait_bar(&b_kf[n % KR], ((n / KR) - 1) & 1u, c.stop, x.wait_ns)));
                 if (!ok) break;
                 uint8_t* gk = gK + (n % KR) * Sh::kK;
 #pragma unroll
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 const uint8_t* next = tile_at(id);
                 if (t + 1 < T) load_k(next);
                 // V, transposed, once P V of the slot's last page has ended
-                if (n >= VR) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[n % VR], ((n / VR) - 1) & 1u, c.stop));
+                if (n >= VR) ok = __all_sync(0xffffffffu, wait_bar(&b_pv[n % VR], ((n / VR) - 1) & 1u, c.stop, x.wait_ns));
                 if (!ok) break;
                 uint8_t* gv = gV + (n % VR) * Sh::kV;
 #pragma unroll
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                     e = vexp;
                 }
                 if (n >= kTileScales)
-                    ok = __all_sync(0xffffffffu, wait_bar(&b_scf[sl], ((n / kTileScales) - 1) & 1u, c.stop));
+                    ok = __all_sync(0xffffffffu, wait_bar(&b_scf[sl], ((n / kTileScales) - 1) & 1u, c.stop, x.wait_ns));
                 if (!ok) break;
                 const float up = pow2(e);
                 bool any = false;
@@ -716,8 +717,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
             const auto pv = [&](int t) {
                 const uint32_t n = gt + t;
                 const int st = n & 1;
-                if (!wait_bar(&b_v[n % VR], (n / VR) & 1u, c.stop) ||
-                    !wait_bar(&b_p[st], (n >> 1) & 1u, c.stop))
+                if (!wait_bar(&b_v[n % VR], (n / VR) & 1u, c.stop, x.wait_ns) ||
+                    !wait_bar(&b_p[st], (n >> 1) & 1u, c.stop, x.wait_ns))
                     return false;
                 tc_fence_after();
                 const uint32_t dv = (uint32_t)tc_sdesc_sw128(sV + (n % VR) * Sh::kV), pa = tmem + Sh::kS + st * KT;
@@ -728,14 +729,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
                 mma_commit(&b_pv[n % VR]);
                 return true;
             };
-            if (!wait_bar(&b_q, seg & 1u, c.stop)) ok = false;
+            if (!wait_bar(&b_q, seg & 1u, c.stop, x.wait_ns)) ok = false;
             int done = 0, asked = 0;                     // tiles whose P V and whose Q K have been issued
             for (int t = 0; ok && t < T; t++) {
                 const uint32_t n = gt + t;
                 const int st = n & 1;
-                if (!wait_bar(&b_k[n % KR], (n / KR) & 1u, c.stop) ||
+                if (!wait_bar(&b_k[n % KR], (n / KR) & 1u, c.stop, x.wait_ns) ||
                     // the stage's P of tile t - 2 has been used
-                    (t >= 2 && !wait_bar(&b_pv[(n - 2) % VR], ((n - 2) / VR) & 1u, c.stop))) {
+                    (t >= 2 && !wait_bar(&b_pv[(n - 2) % VR], ((n - 2) / VR) & 1u, c.stop, x.wait_ns))) {
                     ok = false;
                     break;
                 }

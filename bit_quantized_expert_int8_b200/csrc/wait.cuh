@@ -54,12 +54,12 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parit
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* status, unsigned long long bound) {
     if (mbar_try_wait_long(bar, parity)) return true;
     const unsigned long long t0 = gtimer_ns();
     while (!mbar_try_wait_long(bar, parity)) {
         const unsigned long long el = gtimer_ns() - t0;
-        if (el > kWaitNs) { fused_fail(status); return false; }
+        if (el > bound) { fused_fail(status); return false; }
         if (el > kAbortCheckNs && fused_aborted(status)) return false;
     }
     return true;

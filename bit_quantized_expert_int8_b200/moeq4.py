@@ -38,7 +38,7 @@ EXPORTS = ("moe_ctx_create", "moe_ctx_destroy", "moe_ctx_check", "moe_ctx_trace"
            "moe_router_topk_noalloc", "moe_set_mma_min_tokens", "moe_set_wait_ns",
            "moe_store_stride", "moe_store_open", "moe_store_close", "moe_store_read",
            "moe_store_stats",
-           "moe_kv_page_bytes", "moe_kv_create", "moe_kv_destroy", "moe_kv_check",
+           "moe_kv_page_bytes", "moe_kv_create", "moe_kv_destroy", "moe_kv_check", "moe_kv_set_wait_ns",
            "moe_kv_append_q4", "moe_kv_read_q4", "moe_attn_q4", "moe_kv_evict")
 
 
@@ -140,6 +140,7 @@ def load() -> ctypes.CDLL:
         "moe_kv_create": ([ctypes.POINTER(CMoeKvConfig), ctypes.POINTER(P)], i32),
         "moe_kv_destroy": ([P], i32),
         "moe_kv_check": ([P, P], i32),
+        "moe_kv_set_wait_ns": ([P, ctypes.c_ulonglong], i32),
         "moe_kv_append_q4": ([P, P, P, P, i64, P, i64, P], i32),
         "moe_kv_read_q4": ([P, P, P, P, i64, P, i64, P], i32),
         "moe_attn_q4": ([P, P, P, P, i64, ctypes.c_float, i32, i32, P, i64, P, P], i32),
@@ -518,6 +519,11 @@ def moe_kv_check(kv, stream=None):
     """Synchronise and raise MoeError if a kernel of this context met a length,
     row start or page index outside its limits since the last check."""
     _check(load().moe_kv_check(kv.handle, _stream(stream)))
+
+
+def moe_kv_set_wait_ns(kv, ns: int):
+    """moe_kv_set_wait_ns: bound of every device wait of the context's attention calls (ns)."""
+    _check(load().moe_kv_set_wait_ns(kv.handle, int(ns)))
 
 
 def _kv_rows_call(fn, kv, cache, batch, k, v, stream):

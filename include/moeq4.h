@@ -577,8 +577,16 @@ int moe_kv_destroy(moe_kv *kv);
 
 /* Synchronises `stream`; MOE_ERR_INVALID_ARG if a kernel of this context met
  * a length, row start or page index outside its limits since the last check,
- * MOE_ERR_TIMEOUT if a bounded wait inside an attention call gave up. */
+ * MOE_ERR_TIMEOUT if a bounded wait inside an attention call gave up: outputs
+ * (and scores) of the attention calls since then are not valid. */
 int moe_kv_check(moe_kv *kv, moe_stream_t stream);
+
+/* Bound of every device wait inside this context's attention calls, in
+ * nanoseconds (default 2e9).  When a wait runs out the kernel records
+ * MOE_ERR_TIMEOUT and leaves; moe_kv_check reports it.  Holds for later calls
+ * (a captured call keeps the bound it was captured with).  Host call, no device
+ * work.  Returns MOE_ERR_INVALID_ARG outside 1e3 .. 6e10 ns. */
+int moe_kv_set_wait_ns(moe_kv *kv, unsigned long long ns);
 
 /* Quantises the call's new rows into their entries: per row, kv head and
  * group of 64 columns, scale = fp16((max - min) / 15), bias = fp16(min),

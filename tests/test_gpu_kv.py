@@ -829,6 +829,24 @@ def test_first_call_captured():
     moeq4.moe_kv_check(c.kv)
 
 
+def test_bounded_wait_gives_up_and_context_recovers():
+    """With a bound of 1 us the tile kernel's waits run out before the first page has
+    been converted: it leaves, the check tells once, and the next call is right."""
+    c = Case(78, 128, 16, 4, [3000, 2000], [128, 100], state=True)
+    q = c.queries()
+    ref = c.reference(q, 0.09)
+    refused(moeq4.MOE_ERR_INVALID_ARG, moeq4.moe_kv_set_wait_ns, c.kv, 999)
+    refused(moeq4.MOE_ERR_INVALID_ARG, moeq4.moe_kv_set_wait_ns, c.kv, 60_000_000_001)
+    moeq4.moe_kv_set_wait_ns(c.kv, 1000)
+    out = torch.zeros((c.n_rows, 16, 128), dtype=torch.float16, device=DEV)
+    moeq4.moe_attn_q4(c.kv, c.cache, c.batch, cu(q), out, scale=0.09)
+    refused(moeq4.MOE_ERR_TIMEOUT, moeq4.moe_kv_check, c.kv)
+    moeq4.moe_kv_check(c.kv)                                     # reported once
+    moeq4.moe_kv_set_wait_ns(c.kv, 2_000_000_000)
+    out, lse = c.attend(q, 0.09, weights=True)
+    close(out, lse, ref)
+
+
 def test_queries_and_outputs_in_the_same_rows():
     c = Case(70, 128, 8, 2, [300, 90], [1, 40])
     q = c.queries()
