@@ -448,8 +448,16 @@ extern "C" int moe_kv_evict(moe_kv* kv, const MoeKvCache* cache, int n_seqs, int
     if (!kv_al(new_lens, 4)) return kv_fail(MOE_ERR_ALIGNMENT, "%s: misaligned new_lens", who);
     if (budget < 1 || n_recent < 0 || n_recent > budget)
         return kv_fail(MOE_ERR_INVALID_ARG, "%s: need 0 <= n_recent <= budget, budget >= 1", who);
-    if (new_lens < cache->lens + n_seqs && cache->lens < new_lens + n_seqs)
-        return kv_fail(MOE_ERR_INVALID_ARG, "%s: new_lens overlaps lens", who);
+    // the first CTA to run writes new_lens while others still read these
+    const size_t per_seq = (size_t)kv->cfg.n_kv_heads * kv->cfg.max_pages * kKvPage;
+    const struct { const void* p; size_t words; } in[] = {{cache->lens, 1}, {cache->seen, 1},
+                                                          {cache->page_table, (size_t)kv->cfg.max_pages},
+                                                          {cache->score, per_seq}, {cache->pos, per_seq}};
+    for (const auto& b : in) {
+        const uintptr_t p = (uintptr_t)b.p, q = (uintptr_t)new_lens;
+        if (q < p + 4 * b.words * n_seqs && p < q + 4 * (size_t)n_seqs)
+            return kv_fail(MOE_ERR_INVALID_ARG, "%s: new_lens overlaps another buffer of the cache", who);
+    }
     if (kv->cfg.max_pages > 8192)
         return kv_fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: max_pages=%d above 8192", who, kv->cfg.max_pages);
     KV_TRY(kv_check_device(kv, who));

@@ -644,7 +644,8 @@ int moe_attn_q4(moe_kv *kv, const MoeKvCache *cache, const MoeKvBatch *batch, co
  * order of entries is no longer the order of tokens.  (Attention needs no
  * order, and the rows of the next call still stand behind all others; a
  * window then counts entries, not tokens.)
- *   new_lens device int32 [n_seqs] = min(lens[s], budget); must not overlap lens
+ *   new_lens device int32 [n_seqs] = min(lens[s], budget); must not overlap the
+ *            cache's lens, seen, page_table, score or pos
  * Needs score, pos and seen, 1 <= budget, 0 <= n_recent <= budget and
  * max_pages <= 8192. */
 int moe_kv_evict(moe_kv *kv, const MoeKvCache *cache, int n_seqs, int budget, int n_recent,

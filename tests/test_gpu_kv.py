@@ -942,6 +942,16 @@ def test_refusals():
     moeq4.moe_kv_check(c.kv)
 
 
+def test_evict_refuses_new_lens_over_what_it_reads():
+    c = Case(79, 128, 4, 2, [100, 50], [1, 1], state=True)
+    for name in ("seen", "table", "score", "pos"):
+        over = c.g[name].view(torch.int32).view(-1)
+        for part in (over[:2], over[-2:]):
+            refused(moeq4.MOE_ERR_INVALID_ARG, moeq4.moe_kv_evict, c.kv, c.cache, 2, 10, 1, part)
+    for name in ("seen", "table", "score", "pos", "pages"):
+        assert np.array_equal(c.g[name].cpu().numpy(), getattr(c, name))
+
+
 @pytest.mark.parametrize("rows", [[1, 2], [40, 70]])
 @pytest.mark.parametrize("what", ["page", "negative page", "start", "start past rows", "max_q", "long", "negative len"])
 def test_bad_device_values_are_reported_and_skipped(what, rows):
