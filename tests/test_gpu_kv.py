@@ -197,6 +197,56 @@ def test_window_with_rows_before_the_first_entry(Hq, lens, rows, window):
     assert (np.abs(got - want) <= 1e-4 * ref[2] + 2.0 ** -23 * np.abs(want) + 1e-6).all(), np.abs(got - want).max()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,lens,rows", [
+    (128, 16, 4, [5000, 3000], [1, 1]), (256, 8, 4, [4000], [1]), (64, 8, 4, [4000], [4]),
+    (128, 8, 4, [3000], [20]), (128, 8, 4, [3000], [100]), (256, 4, 4, [2500], [130]), (64, 8, 4, [2500], [120])])
+def test_precision_over_long_sequences(D, Hq, Hkv, lens, rows):
+    """Norms of the errors, where a bound on each element has to allow for all of an
+    element's roundings at once.  Output: two roundings to fp16 (p s or V, and the output
+    itself), each 2^-11 sqrt(1/3 / 2.164) = 1.92e-4 of a value with evenly distributed log,
+    2.7e-4 together; a third one would make it 3.3e-4.  lse (8 to 10): a score's partial
+    sums, below 40 * 0.09, are rounded to 2^-24 of that a few dozen times, 1e-6 to 5e-6 in
+    all.  Weights: exp of that error."""
+    c = Case(90 + D + sum(rows), D, Hq, Hkv, lens, rows, state=True)
+    c.score[:] = 0
+    c.upload()
+    q = c.queries()
+    ref = c.reference(q, 1 / math.sqrt(D))
+    out, lse = c.attend(q, 1 / math.sqrt(D), weights=True)
+    got = c.g["score"].cpu().numpy().astype(np.float64)
+
+    def off(x, y):
+        return np.linalg.norm(x - y) / np.linalg.norm(y)
+
+    assert off(out, ref[0]) <= 3.2e-4
+    assert off(lse, ref[1]) <= 5e-7
+    assert off(got, ref[2]) <= 2e-6
+
+
+def test_rows_of_the_first_sequence_begin_later():
+    """row_start need not begin at 0: rows before it belong to nobody."""
+    for rows in ([1, 2], [40, 50]):
+        c = Case(83, 128, 8, 2, [200, 90], rows, spare_rows=6, state=True)
+        q, n = c.queries(), sum(rows)
+        kv = c.rng.standard_normal((2, c.n_rows, 2, 128)).astype(np.float16)
+        batch = moeq4.KvBatch(c.kv, cu(c.start + 3), c.n_rows, max(rows))
+        moeq4.moe_kv_append_q4(c.kv, c.cache, batch, cu(kv[0]), cu(kv[1]))
+        for s in range(2):
+            for i in range(rows[s]):
+                r, at = c.start[s] + 3 + i, c.lens[s] - rows[s] + i
+                kv_ref.append(c.pages, c.table[s], at, kv[0][r], kv[1][r])
+        assert np.array_equal(c.g["pages"].cpu().numpy(), c.pages)
+        ref = c.reference(np.roll(q, -3, axis=0), 0.09)
+        c.batch = batch
+        out, lse = c.attend(q, 0.09)
+        close(out[3:], lse[3:], ref, n)
+        assert (out[:3] == 7).all() and (out[n + 3:] == 7).all() and (lse[:3] == 7).all() and (lse[n + 3:] == 7).all()
+        back = torch.full((2, c.n_rows, 2, 128), 7.0, dtype=torch.float16, device=DEV)
+        moeq4.moe_kv_read_q4(c.kv, c.cache, batch, back[0], back[1])
+        moeq4.moe_kv_check(c.kv)
+        assert (back[:, :3] == 7).all() and (back[:, n + 3:] == 7).all() and (back[:, 3:n + 3] != 7).any()
+
+
 def test_long_sequences_and_split_work():
     c = Case(21, 128, 16, 4, [9000, 3, 2500, 640], [1, 1, 1, 1], state=True)
     q = c.queries()
@@ -340,6 +390,82 @@ def scale_v(pages, table, j, factor, groups=(0, 1)):
         sb = pages[table[j // 64], :, o:o + 4].copy().view(np.float16).astype(np.float64)
         with np.errstate(over="ignore"):
             pages[table[j // 64], :, o:o + 4] = (sb * factor).astype(np.float16).view(np.uint8)
+
+
+@pytest.mark.parametrize("rows,window", [([1, 1], 0), ([9, 40], 20), ([70, 80], 0), ([130, 140], 30)])
+def test_masked_entries_add_no_weight(rows, window):
+    """As above with weights: NaN scales outside the rows' range leave scores alone too."""
+    c = Case(26, 128, 8, 2, [150, 201], rows, extra_pages=2, state=True)
+    q = c.queries()
+    ref = c.reference(q, 0.09, window)
+    ng = 2
+    for s in range(c.n):
+        first = c.lens[s] - rows[s]
+        lo = max(0, first - window + 1) if window else 0
+        for j in [*range(lo), *range(int(c.lens[s]), c.cap)]:
+            for o in range(2048 * ng + (j % 64) * 4, 4608 * ng, 256):
+                if o % (2304 * ng) >= 2048 * ng:
+                    c.pages[c.table[s, j // 64], :, o:o + 4] = np.array([np.nan, np.inf], np.float16).view(np.uint8)
+    c.upload()
+    out, lse = c.attend(q, 0.09, window, weights=True)
+    close(out, lse, ref)
+    want = c.score.astype(np.float64) + ref[2]
+    got = c.g["score"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= 1e-4 * ref[2] + 2.0 ** -23 * np.abs(want) + 1e-6).all()
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("rows", [30, 80, 200])
+def test_nan_reaches_only_the_rows_that_see_it_with_many_rows(rows, what):
+    """A row appended with NaN in kv head 1: that head's rows behind it get NaN (in V's
+    group of 64 columns alone), all others what they would get anyway."""
+    c = Case(27, 128, 4, 2, [300], [rows], state=True)
+    q = c.queries()
+    at, i = 300 - rows // 2, rows - rows // 2                    # row i stands at entry `at`
+    new = c.rng.standard_normal((2, 2, 128)).astype(np.float16)
+    kv_ref.append(c.pages, c.table[0], at, *new)
+    ref = c.reference(q, 0.09)
+    new[0 if what == "k" else 1][1, 3] = np.nan
+    kv_ref.append(c.pages, c.table[0], at, *new)
+    c.upload()
+    out, lse = c.attend(q, 0.09, weights=True)
+    cols = slice(0, 128 if what == "k" else 64)
+    assert np.isnan(out[i:, 2:, cols]).all()
+    out[i:, 2:, cols] = ref[0][i:, 2:, cols]
+    if what == "k":
+        assert np.isnan(lse[i:, 2:]).all()
+        lse[i:, 2:] = ref[1][i:, 2:]
+    close(out, lse, ref)
+    got = c.g["score"].cpu().numpy()[0].astype(np.float64)
+    want = c.score[0].astype(np.float64) + ref[2][0]
+    assert (np.abs(got - want)[0] <= 1e-4 * ref[2][0, 0] + 2.0 ** -23 * want[0] + 1e-6).all()
+    if what == "k":
+        assert np.isnan(got[1, :300]).all()                      # a weight of every entry is NaN
+    else:
+        assert (np.abs(got - want)[1] <= 1e-4 * ref[2][0, 1] + 2.0 ** -23 * want[1] + 1e-6).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,rows", [(128, 16, 8, 256), (64, 16, 16, 130), (256, 8, 8, 200)])
+def test_v_that_grows_and_shrinks_between_pages(D, Hq, Hkv, rows):
+    """V a thousand times larger, and smaller, from one page to the next, with many rows
+    and several pages a CTA: what has been summed follows the unit that V is held in."""
+    c = Case(80 + D, D, Hq, Hkv, [2000], [rows])
+    ng = D // 64
+    factor = 10.0 ** np.array([0, -3, 0, 2, -1, 3, 0, -3])       # V of 1e-3 to 1e3
+    for p in range(c.max_pages):
+        o = 2304 * ng + 2048 * ng
+        t = c.pages[c.table[0, p], :, o:]
+        t[:] = (t.copy().view(np.float16).astype(np.float64) * factor[p % 8]).astype(np.float16).view(np.uint8)
+    c.upload()
+    q = c.queries()
+    ref = c.reference(q, 0.7 / math.sqrt(D))
+    out, lse = c.attend(q, 0.7 / math.sqrt(D))
+    # the terms are as large as the largest V, 1000
+    assert (np.abs(out - ref[0]) <= 2.0 ** -11 * (np.abs(ref[0]) + ref[3]) + 2.0 ** -25 + 1e-4 * 1000).all()
+    assert (np.abs(lse - ref[1]) <= 1e-4).all()
+    # as a whole: two roundings to fp16, each sqrt(E e^2 / E x^2) = 2^-11 sqrt(1/3 / 2.164) = 1.92e-4
+    # of a value with evenly distributed log, 2.7e-4 together; three would be 3.3e-4
+    assert np.linalg.norm(out - ref[0]) <= 3.2e-4 * np.linalg.norm(ref[0])
 
 
 @pytest.mark.parametrize("bad", [np.inf, np.nan])
