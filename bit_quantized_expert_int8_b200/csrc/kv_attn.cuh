@@ -371,8 +371,7 @@ __device__ __forceinline__ void split_block(SplitAcc<NG, RT>& A, uint32_t kb, ui
 #pragma unroll
                 for (int z = 0; z < RT; z++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                    {
+                    for (int k = 0; k < 4; k++) {
                         const float v = p[z][4 * b + k] * h2f(sb[g][k]).x;
                         if (seen(z, k)) mx = fmaxf(mx, fabsf(fmaf(v, 0.f, v)));  // v, or NaN, which fmaxf passes over
                     }
