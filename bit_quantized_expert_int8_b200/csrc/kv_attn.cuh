@@ -169,14 +169,15 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 //
 // What bounds it is instruction issue and latency, about 690 instructions per 32
 // entries of 128 columns and three warps a scheduler (54 % of the issue slots): 64
-// tokens with up to 16,384 entries take 169 us (3.6 TB/s of the cache, 0.56 of the
-// copy rate), one with 131,072 50 us (3.0 TB/s, the start and the join of the parts
+// tokens with up to 16,384 entries take 162 to 169 us, as their lengths fall (3.6 TB/s of
+// the cache, 0.56 of the copy rate), one with 131,072 50 us (3.0 TB/s, the start and the join of the parts
 // included; the loop alone streams 4.6 TB/s).
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
-// Ring stages (and CTAs per SM below): 3 stages with 2 CTAs take 100 us for 64 tokens
-// with a window of 1024 (heads of 256), 2 with 3 take 84; 4 CTAs of 128 registers 5 %
-// more than 3 over long sequences of heads of 128.
+// Ring stages.  64 tokens with a window of 1024 (heads of 256): 3 stages, which leave
+// room for one CTA per SM, 100 us, 2 stages and two CTAs 83.  64 tokens of up to 16,384
+// entries (heads of 128): 3 stages and two CTAs 171 us, 2 and three 169, 4 CTAs of 128
+// registers 5 % more.
 constexpr int kSplitStages = 2;
 // An item's start and end in pages.  64 tokens with up to 16,384 entries: 0 184 us, 2
 // to 8 alike (169).
@@ -199,7 +200,9 @@ struct SplitShape {
     static constexpr int kJoin = kSplitWarps * kRows * kJoinRow * 4; // the warps' sums, over the ring
     static constexpr int kQ = NG * 4 * 32 * 16;                      // query operand, 16 rows (zeros behind 8)
     static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
-    static constexpr int kCtas = NG * RT <= 4 ? 3 : 2;               // per SM
+    // CTAs per SM that the registers are bounded for; as many fit, but for <4, 1>, where
+    // 82 KB of shared memory a CTA let two in
+    static constexpr int kCtas = NG * RT <= 4 ? 3 : 2;
 };
 
 struct SplitArgs {

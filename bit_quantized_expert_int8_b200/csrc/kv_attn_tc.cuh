@@ -12,12 +12,14 @@
 // lse, 1.8e-7 of it instead of 0.9e-7 with heads of 256).  (With the raw codes as operands
 // and the groups' scales folded in by the softmax threads, as the few-row kernel
 // does it, every thread reads every entry's scales from shared memory: 512
-// 16-byte broadcasts a tile, 427 us against 334 at 4 chunks of 512.)  p enters as
+// 16-byte broadcasts a tile, 427 us at 4 chunks of up to 512 rows against 360 when two
+// operands replaced them; now 338 to 387, as the chunks' lengths fall.)  p enters as
 // hi and remainder too; V is rounded to fp16 once, a relative 2^-12 on average, as
 // the output is (one more rounding, of p, would make the error 1.7 times that of
-// the output's own rounding instead of 1.4).  K and V are scaled by powers of two, so that no value leaves
-// fp16's range: K's (per page) divides the softmax scale, V's (held until a page
-// exceeds it) leaves at the end.  The row maximum moves only when it grows by more
+// the output's own rounding instead of 1.4).  K and V are scaled by powers of two, so
+// that no value leaves fp16's range: K's (per page) divides the softmax scale, V's (held
+// until a page exceeds it) leaves at the end; small V are held to 2^-31 of the largest
+// that a row of the tile sees.  The row maximum moves only when it grows by more
 // than 2^8, and only then is O rescaled.  Groups of V that are not finite enter as
 // zeros; rows that see one get a NaN in its columns at the end, so that masked
 // rows (p = 0) stay clean.
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const TileArgs x)
 // of its tile, one per lane, 64 columns a CTA, 8 a warp, eight parts at a time with
 // all their loads in flight (the weights first and then 16 columns a warp, two
 // passes where heads are wide, made a chunk of 128 rows over 4,096 entries of 256
-// columns 60 us; now 52).
+// columns 60 us; now 53).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 8;
 
